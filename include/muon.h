@@ -1,7 +1,9 @@
 /*
- * muon.h -- C ABI of the MI355X (gfx950) Muon optimizer step.
+ * muon.h -- C ABI of the MI355X (gfx950) Muon optimizer step, and of the layer
+ * operators that make the gradients it takes (layer norm, the linear layer's
+ * products, 8-bit activation checkpoints; see "the layer operators" below).
  *
- * One call performs, for every 2-D weight in a list, the Muon step the speedrun
+ * One muon_step call performs, for every 2-D weight in a list, the Muon step the speedrun
  * pages describe:
  *
  *   m'  = beta * m + g                      momentum, no dampening
@@ -45,7 +47,7 @@
 extern "C" {
 #endif
 
-#define MUON_ABI_VERSION 6
+#define MUON_ABI_VERSION 7
 
 typedef enum muon_status {
     MUON_OK = 0,
@@ -165,6 +167,123 @@ typedef struct muon_adamw_hparams {
     int32_t step;              /* 1-based step count t of this update (bias corrections 1 - beta^t) */
 } muon_adamw_hparams;
 
+/* ---- the layer operators: what makes the gradients the steps above take ---- */
+
+/* 8-bit activation checkpoint of a rows x cols matrix.  The 32 columns
+ * [32 j, 32 j + 32) of a row (fewer at its end) form a group that shares one
+ * exponent byte: element (r, c) stands for
+ *
+ *   codes[r * ld_codes + c] * 2^(exponents[r * ld_exponents + c / 32] - 127).
+ *
+ * The encoder takes the smallest power of two, not under 2^-126, that keeps
+ * every code of the group within -127..127, and rounds to nearest even: an
+ * element is off by at most half a step, 2^-7 of its group's largest magnitude
+ * (2^-8 at best).  Decoding is exact in bfloat16 and float32.  A group holding
+ * an infinity or a NaN gets exponent byte 255 and codes 0: all of it decodes to
+ * NaN. */
+typedef struct muon_act8 {
+    int8_t  *codes;            /* rows x cols */
+    uint8_t *exponents;        /* rows x ceil(cols / 32) */
+    int64_t  ld_codes;         /* >= cols */
+    int64_t  ld_exponents;     /* >= ceil(cols / 32) */
+} muon_act8;
+#define MUON_ACT8_GROUP 32
+
+typedef enum muon_activation {
+    MUON_ACT_NONE = 0,
+    MUON_ACT_GELU = 1,         /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    MUON_ACT_RELU_SQ = 2       /* max(z, 0)^2 */
+} muon_activation;
+
+/* How a linear layer's weight is stored; either is a muon_matrix for muon_step. */
+typedef enum muon_weight_layout {
+    MUON_W_IN_OUT = 0,         /* in x out */
+    MUON_W_OUT_IN = 1          /* out x in */
+} muon_weight_layout;
+
+/* Arguments of muon_layernorm_forward.  Pointers noted "optional" may be NULL. */
+typedef struct muon_layernorm_args {
+    const void *x;             /* rows x cols, `dtype` */
+    const void *gain;          /* cols, `param_dtype` */
+    const void *bias;          /* cols, `param_dtype`; optional */
+    void       *y;             /* rows x cols, `dtype` */
+    float      *mean;          /* rows; optional */
+    float      *rstd;          /* rows; optional */
+    muon_act8   y8;            /* y's 8-bit checkpoint, of y before its rounding; codes NULL = none */
+    int64_t     rows, cols;    /* rows >= 0, 1 <= cols <= 2^20 */
+    int64_t     ld_x, ld_y;
+    int32_t     dtype, param_dtype;   /* muon_dtype */
+    float       eps;           /* added to the variance, >= 0, finite */
+    int32_t     reserved;      /* must be 0 */
+} muon_layernorm_args;
+
+/* Arguments of muon_layernorm_backward. */
+typedef struct muon_layernorm_grad_args {
+    const void  *dy;           /* rows x cols, `dtype` */
+    const void  *x;            /* rows x cols, `dtype`: the forward pass's input */
+    const void  *gain;         /* cols, `param_dtype` */
+    const float *mean, *rstd;  /* rows: as the forward pass wrote them */
+    const void  *add;          /* rows x cols, `dtype`, added to dx (the residual path's gradient); optional;
+                                  may be dx itself (same leading dimension) */
+    void        *dx;           /* rows x cols, `dtype` */
+    void        *dgain;        /* cols, `param_dtype` */
+    void        *dbias;        /* cols, `param_dtype`; optional */
+    int64_t      rows, cols;
+    int64_t      ld_dy, ld_x, ld_add, ld_dx;
+    int32_t      dtype, param_dtype;
+    int32_t      accumulate;   /* 1: dgain and dbias are added to */
+    int32_t      reserved;     /* must be 0 */
+} muon_layernorm_grad_args;
+
+/* Arguments of muon_linear_forward. */
+typedef struct muon_linear_args {
+    const void *x;             /* rows x in, `dtype` */
+    const void *w;             /* in x out or out x in (w_layout), `dtype` */
+    const void *bias;          /* out, `bias_dtype`; optional */
+    const void *residual;      /* rows x out, `dtype`, added after the activation; optional; may be y itself */
+    void       *y;             /* rows x out, `dtype` */
+    void       *z;             /* rows x out, `dtype`: receives x W + bias; optional */
+    muon_act8   z8;            /* or its 8-bit checkpoint, taken before any rounding; codes NULL = none */
+    int64_t     rows, in, out; /* rows >= 0; 1 <= in, out <= 2^20 */
+    int64_t     ld_x, ld_w, ld_residual, ld_y, ld_z;
+    int32_t     dtype, bias_dtype;    /* muon_dtype */
+    int32_t     activation;    /* muon_activation */
+    int32_t     w_layout;      /* muon_weight_layout */
+    int32_t     reserved;      /* must be 0 */
+} muon_linear_args;
+
+/* Arguments of muon_linear_grad_input. */
+typedef struct muon_linear_grad_input_args {
+    const void *dy;            /* rows x out, `dtype` */
+    const void *w;             /* as in the forward pass */
+    const void *z;             /* rows x in, `dtype`: the pre-activation behind this layer's input; optional */
+    muon_act8   z8;            /* or its 8-bit checkpoint (read); codes NULL = none */
+    const void *add;           /* rows x in, `dtype`, added last; optional; may be dx itself */
+    void       *dx;            /* rows x in, `dtype` */
+    void       *act_out;       /* rows x in, `dtype`: receives act(z), this layer's input; optional, needs z or z8 */
+    int64_t     rows, in, out;
+    int64_t     ld_dy, ld_w, ld_z, ld_add, ld_dx, ld_act_out;
+    int32_t     dtype;
+    int32_t     activation;    /* of z; MUON_ACT_NONE without z and z8 */
+    int32_t     w_layout;
+    int32_t     reserved;      /* must be 0 */
+} muon_linear_grad_input_args;
+
+/* Arguments of muon_linear_grad_weight. */
+typedef struct muon_linear_grad_weight_args {
+    const void *x;             /* rows x in, `dtype`; or NULL and */
+    muon_act8   x8;            /* its 8-bit checkpoint (read) */
+    const void *dy;            /* rows x out, `dtype` */
+    void       *dw;            /* in x out or out x in (w_layout), `dw_dtype` */
+    void       *db;            /* out, `db_dtype`; optional */
+    int64_t     rows, in, out;
+    int64_t     ld_x, ld_dy, ld_dw;
+    int32_t     dtype, dw_dtype, db_dtype;
+    int32_t     w_layout;
+    int32_t     accumulate;    /* 1: dw and db are added to */
+    int32_t     reserved;      /* must be 0 */
+} muon_linear_grad_weight_args;
+
 /* Version of this header the library was built from (MUON_ABI_VERSION). */
 int muon_abi_version(void);
 
@@ -269,6 +388,62 @@ muon_status muon_orthogonalize(muon_handle *h, const void *in, float *out,
  * MUON_ERR_HIP. */
 muon_status muon_adamw_step(muon_handle *h, const muon_adamw_tensor *tensors, int32_t n,
                             const muon_adamw_hparams *hp, void *stream);
+
+/* Layer norm over the rows of x, enqueued on `stream`:
+ *
+ *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   y = (x - mean) rstd gain + bias
+ *
+ * in float32, y rounded once to its dtype.  mean and rstd are kept for the
+ * backward pass, y8 holds y for the weight gradient of the layer it feeds.
+ *
+ * Conventions of the seven layer operators: every matrix is row-major with a
+ * leading dimension in elements; any alignment of the element type and any
+ * size is taken (16-byte aligned rows of whole 16-byte chunks run fastest);
+ * rows == 0 enqueues nothing, except that the gradients of parameters are then
+ * zeroed (or left, with accumulate).  Nothing but the named outputs is
+ * written: a leading dimension's padding keeps its values.  Outputs may not be
+ * inputs or each other except where noted (base addresses are compared).
+ * Results do not depend on timing: the same call gives the same bits.  They
+ * are not among the profiled roles.  Workspaces belong to the handle, grow to
+ * what the largest call needs and are kept until muon_destroy; calls on one
+ * handle share them and must be ordered, like those of muon_step.  A call
+ * captured into a HIP graph must find its workspace large enough, so a call of
+ * the same sizes must have run once outside capture (MUON_ERR_INVALID_ARG
+ * otherwise); a workspace that a graph uses is never freed or moved while the
+ * handle lives.  Errors: MUON_ERR_INVALID_ARG (a null handle, argument struct
+ * or required pointer, a size or leading dimension out of range, aliasing, an
+ * unknown activation or weight layout, both z and z8, act_out without either, an
+ * activation without either in muon_linear_grad_input, flags other than 0 and
+ * 1, reserved != 0), MUON_ERR_DTYPE, MUON_ERR_OOM, MUON_ERR_HIP. */
+muon_status muon_layernorm_forward(muon_handle *h, const muon_layernorm_args *args, void *stream);
+
+/* Its gradient: with xh = (x - mean) rstd and a = dy gain,
+ *
+ *   dx = rstd (a - sum a / cols - xh sum (a xh) / cols) + add
+ *   dgain = sum over rows of dy xh;  dbias = sum over rows of dy */
+muon_status muon_layernorm_backward(muon_handle *h, const muon_layernorm_grad_args *args, void *stream);
+
+/* y = act(x W + bias) + residual: one matrix product with its epilogue, sums in
+ * float32, each output rounded once.  W is in x out (W(i, o) = w[i * ld_w + o])
+ * or out x in (w[o * ld_w + i]).  Sums of few rows or few columns are split
+ * over workgroups along `in` and joined by a second kernel. */
+muon_status muon_linear_forward(muon_handle *h, const muon_linear_args *args, void *stream);
+
+/* dx = (dy W^T) act'(z) + add: the gradient at the pre-activation z of the layer
+ * before (act its activation), or at this layer's input without z and z8. */
+muon_status muon_linear_grad_input(muon_handle *h, const muon_linear_grad_input_args *args, void *stream);
+
+/* dw = x^T dy (as w is stored), db = the column sums of dy: what muon_step and
+ * muon_adamw_step take as gradients. */
+muon_status muon_linear_grad_weight(muon_handle *h, const muon_linear_grad_weight_args *args, void *stream);
+
+/* The 8-bit checkpoint `q` of a rows x cols matrix x (dtype, leading dimension
+ * ld_x), and back: y = what q stands for, in `dtype`. */
+muon_status muon_act_encode(muon_handle *h, const void *x, int64_t rows, int64_t cols, int64_t ld_x,
+                            int32_t dtype, const muon_act8 *q, void *stream);
+muon_status muon_act_decode(muon_handle *h, const muon_act8 *q, void *y, int64_t rows, int64_t cols,
+                            int64_t ld_y, int32_t dtype, void *stream);
 
 /* Frobenius norms ||u||_F of the orthogonalised inputs of the most recent
  * muon_step (as enqueued: read after that step's kernels), one per plan entry (a blocked matrix has one per block, row-major)

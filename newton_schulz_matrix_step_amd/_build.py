@@ -21,7 +21,8 @@ LIB_NAME = "libmuon_mi355x.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
-SOURCES = ["muon_api.cpp", "muon_kernels.hip", "adamw_kernels.hip", "muon_static.hip"]
+SOURCES = ["muon_api.cpp", "muon_kernels.hip", "adamw_kernels.hip", "muon_static.hip",
+           "layer_api.cpp", "norm_kernels.hip", "linear_kernels.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -22,6 +22,7 @@
 #pragma GCC visibility push(default)
 #include "../../include/muon.h"
 #pragma GCC visibility pop
+#include "layer_internal.hpp"
 #include "muon_internal.hpp"
 
 using namespace muon;
@@ -159,10 +160,7 @@ struct Pending {
 
 }  // namespace
 
-struct muon_handle {
-    int device = 0;
-    uint32_t flags = 0;
-    std::string err;
+struct muon_handle : muon::HandleBase {
     std::map<std::vector<int64_t>, std::unique_ptr<Plan>> plans;
     std::map<std::vector<int64_t>, std::unique_ptr<AdamPlan>> adam_plans;
     Plan* last_step = nullptr;   // plan of the latest muon_step (norm readback)
@@ -174,6 +172,8 @@ struct muon_handle {
     int64_t launches[K_NROLES] = {};
     double total_ms[K_NROLES] = {};
 };
+
+muon::HandleBase* muon::handle_base(muon_handle* h) { return h; }
 
 namespace {
 
@@ -1269,6 +1269,7 @@ int64_t muon_workspace_bytes(const muon_handle* h) {
     if (!h) return 0;
     int64_t b = 0;
     for (const auto& kv : h->plans) b += int64_t(kv.second->ws_bytes);
+    if (h->layers) b += h->layers->workspace_bytes();
     return b;
 }
 
@@ -1279,6 +1280,7 @@ muon_status muon_destroy(muon_handle* h) {
         (void)hipDeviceSynchronize();
         for (auto& kv : h->plans) free_plan(*kv.second);
         for (auto& kv : h->adam_plans) free_adam_plan(*kv.second);
+        h->layers.reset();
         for (const Pending& p : h->pending) {
             (void)hipEventDestroy(p.a);
             (void)hipEventDestroy(p.b);
