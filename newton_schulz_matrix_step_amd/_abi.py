@@ -552,14 +552,14 @@ class Act8:
 
     def __init__(self, codes, exponents):
         import torch
-        if codes.dtype != torch.int8 or exponents.dtype != torch.uint8:
+        if codes.dtype is not torch.int8 or exponents.dtype is not torch.uint8:
             raise ValueError(f"Act8: codes must be int8 and exponents uint8, got {codes.dtype} and {exponents.dtype}")
         if codes.dim() != 2 or exponents.dim() != 2:
             raise ValueError("Act8: codes and exponents must be 2-D")
-        g = -(-int(codes.shape[1]) // MUON_ACT8_GROUP)
-        if tuple(exponents.shape) != (int(codes.shape[0]), g):
-            raise ValueError(f"Act8: exponents have shape {tuple(exponents.shape)}, codes {tuple(codes.shape)} need "
-                             f"{(int(codes.shape[0]), g)}")
+        r, c = codes.shape
+        want = (r, -(-c // MUON_ACT8_GROUP))
+        if exponents.shape != want:
+            raise ValueError(f"Act8: exponents have shape {tuple(exponents.shape)}, codes {tuple(codes.shape)} need {want}")
         self.codes = codes
         self.exponents = exponents
 
@@ -574,7 +574,11 @@ class Act8:
         return self.codes.shape
 
     def _c(self) -> muon_act8:
-        return muon_act8(self.codes.data_ptr(), self.exponents.data_ptr(), _ld2(self.codes), _ld2(self.exponents))
+        q, e = self.codes, self.exponents
+        if q.is_contiguous() and e.is_contiguous():
+            c = q.shape[1]
+            return muon_act8(q.data_ptr(), e.data_ptr(), c, -(-c // MUON_ACT8_GROUP))
+        return muon_act8(q.data_ptr(), e.data_ptr(), _ld2(q), _ld2(e))
 
 
 _NO_ACT8 = muon_act8()
@@ -585,54 +589,100 @@ def _ld2(t) -> int:
     column or row may carry any stride)."""
     if t.dim() != 2:
         raise ValueError("matrices must be 2-D with unit column stride")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    ld, cs = t.stride()
+    rows, cols = t.shape
+    if cs != 1 and cols > 1:
         raise ValueError("matrices must be 2-D with unit column stride")
-    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), int(t.shape[1]))
+    return ld if rows > 1 else max(ld, cols)
 
 
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+class _Torch:
+    """What the layer calls need of torch, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.f32 = torch.float32
+        self.codes = {torch.bfloat16: MUON_BF16, torch.float32: MUON_F32}
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _layer_tensors(what: str, shapes, dtypes):
-    """Check named tensors: ``shapes`` (name, tensor or None, expected shape),
-    ``dtypes`` groups of (name, tensor or None) that share a storage dtype; all
-    on one GPU, which is returned."""
-    import torch
-    for nm, t, shape in shapes:
-        if t is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{what}: {nm} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    for group in dtypes:
-        have = [(nm, t) for nm, t in group if t is not None]
-        for nm, t in have:
-            if t.dtype not in (torch.bfloat16, torch.float32):
-                raise ValueError(f"{what}: {nm} must be bfloat16 or float32, got {t.dtype}")
-            if t.dtype != have[0][1].dtype:
-                raise ValueError(f"{what}: {nm} is {t.dtype}, {have[0][0]} {have[0][1].dtype}")
-    flat = []
-    for _, t, _ in shapes:
-        if isinstance(t, Act8):
-            flat += [t.codes, t.exponents]
-        elif t is not None:
-            flat.append(t)
-    for t in flat:
-        if t.dim() == 1 and t.numel() > 1 and t.stride(0) != 1:
-            raise ValueError(f"{what}: vectors must be contiguous")
-    return _check_device_tensors(what, flat)
+_torch: Optional[_Torch] = None
 
 
-def _stream_on(stream, device) -> int:
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return int(stream.cuda_stream)
+class _Args:
+    """Checks of one layer call's tensors (the C ABI sees only pointers and
+    sizes) and their marshalling.  The first tensor names the GPU that all
+    others must be on.  A contiguous tensor as expected takes the short way
+    through each method; the rest of it names what is wrong."""
 
+    __slots__ = ("what", "device", "device_ok", "torch")
 
-def _f32_vectors(what: str, **ts):
-    import torch
-    for nm, t in ts.items():
-        if t is not None and t.dtype != torch.float32:
-            raise ValueError(f"{what}: {nm} must be float32, got {t.dtype}")
+    def __init__(self, what: str, t):
+        global _torch
+        if _torch is None:
+            _torch = _Torch()
+        self.torch = _torch
+        self.what = what
+        self.device = t.get_device()   # -1: the host
+        self.device_ok = self.device >= 0
+
+    def fail(self, msg: str):
+        raise ValueError(f"{self.what}: {msg}")
+
+    def check(self, nm, t, shape, dt, like=None):
+        if t.shape != shape:
+            self.fail(f"{nm} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype is not dt:
+            self.fail(f"{nm} is {t.dtype}, {like} {dt}" if like else f"{nm} must be {str(dt)[6:]}, got {t.dtype}")
+        if t.get_device() != self.device:
+            self.device_ok = False
+
+    def storage(self, nm, t) -> int:
+        """muon_dtype of a tensor that may be bfloat16 or float32."""
+        c = self.torch.codes.get(t.dtype)
+        if c is None:
+            self.fail(f"{nm} must be bfloat16 or float32, got {t.dtype}")
+        return c
+
+    def matrix(self, nm, t, shape, dt, like):
+        """(pointer, leading dimension); (None, 0) for an absent one."""
+        if t is None:
+            return None, 0
+        if t.shape == shape and t.dtype is dt and t.get_device() == self.device and t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        self.check(nm, t, shape, dt, like)
+        return t.data_ptr(), _ld2(t)
+
+    def vector(self, nm, t, n, dt, like=None):
+        if t is None:
+            return None
+        if t.shape == (n,) and t.dtype is dt and t.get_device() == self.device and t.is_contiguous():
+            return t.data_ptr()
+        self.check(nm, t, (n,), dt, like)
+        if n > 1 and t.stride(0) != 1:
+            self.fail("vectors must be contiguous")
+        return t.data_ptr()
+
+    def act8(self, nm, q, shape):
+        if q is None:
+            return _NO_ACT8
+        if q.codes.shape != shape:
+            self.fail(f"{nm} has shape {tuple(q.codes.shape)}, expected {tuple(shape)}")
+        if q.codes.get_device() != self.device or q.exponents.get_device() != self.device:
+            self.device_ok = False
+        return q._c()
+
+    def rows_cols(self, nm, t):
+        if t.dim() != 2:
+            self.fail(f"{nm} must be 2-D")
+        return t.shape
+
+    def stream(self, stream) -> int:
+        """The given stream, or the current one of the tensors' GPU.  Called
+        last: shapes and dtypes are reported before the device is."""
+        if not self.device_ok:
+            self.fail("tensors must all be on one GPU")
+        return int(stream.cuda_stream) if stream is not None else self.torch.raw_stream(self.device)
 
 
 def _code(what: str, table: dict, value: str, name: str) -> int:
@@ -645,47 +695,44 @@ def muon_layernorm_forward(handle: int, x, gain, bias, y, mean=None, rstd=None, 
                            y8: Optional[Act8] = None, stream=None) -> None:
     """y = layer norm of x's rows (``bias`` may be None); ``mean``, ``rstd``
     (float32, one per row) and ``y8`` (y's 8-bit checkpoint) are written where given."""
-    w = "muon_layernorm_forward"
-    if x.dim() != 2:
-        raise ValueError(f"{w}: x must be 2-D")
-    r, c = (int(v) for v in x.shape)
-    _f32_vectors(w, mean=mean, rstd=rstd)
-    dev = _layer_tensors(w, [("x", x, (r, c)), ("gain", gain, (c,)), ("bias", bias, (c,)), ("y", y, (r, c)),
-                             ("mean", mean, (r,)), ("rstd", rstd, (r,)), ("y8", y8, (r, c))],
-                         [[("x", x), ("y", y)], [("gain", gain), ("bias", bias)]])
-    a = muon_layernorm_args(x.data_ptr(), gain.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(mean), _ptr(rstd),
-                            y8._c() if y8 is not None else _NO_ACT8, r, c, _ld2(x), _ld2(y), _dtype_code(x),
-                            _dtype_code(gain), float(eps), 0)
-    _check(handle, load().muon_layernorm_forward(handle, ctypes.byref(a), _stream_on(stream, dev)))
+    k = _Args("muon_layernorm_forward", x)
+    shape = k.rows_cols("x", x)
+    r, c = shape
+    dt, pdt, f32 = x.dtype, gain.dtype, k.torch.f32
+    dc, pc = k.storage("x", x), k.storage("gain", gain)
+    px, ldx = k.matrix("x", x, shape, dt, "x")
+    py, ldy = k.matrix("y", y, shape, dt, "x")
+    a = muon_layernorm_args(px, k.vector("gain", gain, c, pdt), k.vector("bias", bias, c, pdt, "gain"), py,
+                            k.vector("mean", mean, r, f32), k.vector("rstd", rstd, r, f32), k.act8("y8", y8, shape),
+                            r, c, ldx, ldy, dc, pc, eps, 0)
+    _check(handle, load().muon_layernorm_forward(handle, a, k.stream(stream)))
 
 
 def muon_layernorm_backward(handle: int, dy, x, gain, mean, rstd, dx, dgain, dbias=None, add=None,
                             accumulate: bool = False, stream=None) -> None:
     """dx (+ ``add``, which may be ``dx``), dgain and dbias of the layer norm
     from dy; ``accumulate`` adds to dgain and dbias."""
-    w = "muon_layernorm_backward"
-    if x.dim() != 2:
-        raise ValueError(f"{w}: x must be 2-D")
-    r, c = (int(v) for v in x.shape)
-    _f32_vectors(w, mean=mean, rstd=rstd)
-    dev = _layer_tensors(w, [("x", x, (r, c)), ("dy", dy, (r, c)), ("gain", gain, (c,)), ("mean", mean, (r,)),
-                             ("rstd", rstd, (r,)), ("dx", dx, (r, c)), ("dgain", dgain, (c,)),
-                             ("dbias", dbias, (c,)), ("add", add, (r, c))],
-                         [[("x", x), ("dy", dy), ("dx", dx), ("add", add)],
-                          [("gain", gain), ("dgain", dgain), ("dbias", dbias)]])
-    a = muon_layernorm_grad_args(dy.data_ptr(), x.data_ptr(), gain.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                 _ptr(add), dx.data_ptr(), dgain.data_ptr(), _ptr(dbias), r, c, _ld2(dy), _ld2(x),
-                                 _ld2(add) if add is not None else 0, _ld2(dx), _dtype_code(x), _dtype_code(gain),
-                                 int(bool(accumulate)), 0)
-    _check(handle, load().muon_layernorm_backward(handle, ctypes.byref(a), _stream_on(stream, dev)))
+    k = _Args("muon_layernorm_backward", x)
+    shape = k.rows_cols("x", x)
+    r, c = shape
+    dt, pdt, f32 = x.dtype, gain.dtype, k.torch.f32
+    dc, pc = k.storage("x", x), k.storage("gain", gain)
+    px, ldx = k.matrix("x", x, shape, dt, "x")
+    pdy, lddy = k.matrix("dy", dy, shape, dt, "x")
+    pdx, lddx = k.matrix("dx", dx, shape, dt, "x")
+    pa, lda = k.matrix("add", add, shape, dt, "x")
+    a = muon_layernorm_grad_args(pdy, px, k.vector("gain", gain, c, pdt), k.vector("mean", mean, r, f32),
+                                 k.vector("rstd", rstd, r, f32), pa, pdx, k.vector("dgain", dgain, c, pdt, "gain"),
+                                 k.vector("dbias", dbias, c, pdt, "gain"), r, c, lddy, ldx, lda, lddx, dc, pc,
+                                 1 if accumulate else 0, 0)
+    _check(handle, load().muon_layernorm_backward(handle, a, k.stream(stream)))
 
 
-def _linear_sizes(what: str, w, w_layout: str):
-    if w.dim() != 2:
-        raise ValueError(f"{what}: the weight must be 2-D")
-    _code(what, W_LAYOUTS, w_layout, "w_layout")
-    a, b = (int(v) for v in w.shape)
-    return (b, a) if w_layout == "out_in" else (a, b)
+def _linear_sizes(k: _Args, w, w_layout: str):
+    """(in, out, muon_weight_layout) of a weight."""
+    a, b = k.rows_cols("the weight", w)
+    lay = _code(k.what, W_LAYOUTS, w_layout, "w_layout")
+    return (b, a, lay) if lay else (a, b, lay)
 
 
 def muon_linear_forward(handle: int, x, w, y, bias=None, act: str = "none", residual=None, z_out=None,
@@ -693,22 +740,20 @@ def muon_linear_forward(handle: int, x, w, y, bias=None, act: str = "none", resi
     """y = act(x W + bias) + residual; ``w`` is (in x out) or, with ``w_layout``
     "out_in", (out x in).  ``residual`` may be ``y``.  ``z_out`` (a tensor or an
     Act8) receives the pre-activation x W + bias."""
-    wh = "muon_linear_forward"
-    k, n = _linear_sizes(wh, w, w_layout)
-    if x.dim() != 2:
-        raise ValueError(f"{wh}: x must be 2-D")
-    r = int(x.shape[0])
+    k = _Args("muon_linear_forward", x)
+    i, o, lay = _linear_sizes(k, w, w_layout)
+    r = k.rows_cols("x", x)[0]
+    dt, dc, ac = x.dtype, k.storage("x", x), _code(k.what, ACTIVATIONS, act, "act")
     z8 = z_out if isinstance(z_out, Act8) else None
-    z = None if z8 is not None else z_out
-    dev = _layer_tensors(wh, [("x", x, (r, k)), ("w", w, w.shape), ("bias", bias, (n,)), ("y", y, (r, n)),
-                              ("residual", residual, (r, n)), ("z_out", z_out, (r, n))],
-                         [[("x", x), ("w", w), ("y", y), ("residual", residual), ("z_out", z)], [("bias", bias)]])
-    a = muon_linear_args(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z),
-                         z8._c() if z8 is not None else _NO_ACT8, r, k, n, _ld2(x), _ld2(w),
-                         _ld2(residual) if residual is not None else 0, _ld2(y), _ld2(z) if z is not None else 0,
-                         _dtype_code(x), _dtype_code(bias) if bias is not None else MUON_F32,
-                         _code(wh, ACTIVATIONS, act, "act"), W_LAYOUTS[w_layout], 0)
-    _check(handle, load().muon_linear_forward(handle, ctypes.byref(a), _stream_on(stream, dev)))
+    px, ldx = k.matrix("x", x, (r, i), dt, "x")
+    pw, ldw = k.matrix("w", w, w.shape, dt, "x")
+    py, ldy = k.matrix("y", y, (r, o), dt, "x")
+    pr, ldr = k.matrix("residual", residual, (r, o), dt, "x")
+    pz, ldz = k.matrix("z_out", None if z8 is not None else z_out, (r, o), dt, "x")
+    bc = MUON_F32 if bias is None else k.storage("bias", bias)
+    a = muon_linear_args(px, pw, k.vector("bias", bias, o, bias.dtype) if bias is not None else None, pr, py, pz,
+                         k.act8("z_out", z8, (r, o)), r, i, o, ldx, ldw, ldr, ldy, ldz, dc, bc, ac, lay, 0)
+    _check(handle, load().muon_linear_forward(handle, a, k.stream(stream)))
 
 
 def muon_linear_grad_input(handle: int, dy, w, dx, act: str = "none", z=None, act_out=None, add=None,
@@ -716,64 +761,57 @@ def muon_linear_grad_input(handle: int, dy, w, dx, act: str = "none", z=None, ac
     """dx = (dy W^T) act'(z) + add: the gradient at the pre-activation ``z`` (a
     tensor or an Act8) behind this layer's input, or at the input itself without
     ``z``.  ``act_out`` receives act(z); ``add`` may be ``dx``."""
-    wh = "muon_linear_grad_input"
-    k, n = _linear_sizes(wh, w, w_layout)
-    if dy.dim() != 2:
-        raise ValueError(f"{wh}: dy must be 2-D")
-    r = int(dy.shape[0])
+    k = _Args("muon_linear_grad_input", dy)
+    i, o, lay = _linear_sizes(k, w, w_layout)
+    r = k.rows_cols("dy", dy)[0]
+    dt, dc, ac = dy.dtype, k.storage("dy", dy), _code(k.what, ACTIVATIONS, act, "act")
     z8 = z if isinstance(z, Act8) else None
-    zt = None if z8 is not None else z
-    dev = _layer_tensors(wh, [("dy", dy, (r, n)), ("w", w, w.shape), ("dx", dx, (r, k)), ("z", z, (r, k)),
-                              ("act_out", act_out, (r, k)), ("add", add, (r, k))],
-                         [[("dy", dy), ("w", w), ("dx", dx), ("z", zt), ("act_out", act_out), ("add", add)]])
-    a = muon_linear_grad_input_args(dy.data_ptr(), w.data_ptr(), _ptr(zt), z8._c() if z8 is not None else _NO_ACT8,
-                                    _ptr(add), dx.data_ptr(), _ptr(act_out), r, k, n, _ld2(dy), _ld2(w),
-                                    _ld2(zt) if zt is not None else 0, _ld2(add) if add is not None else 0, _ld2(dx),
-                                    _ld2(act_out) if act_out is not None else 0, _dtype_code(dy),
-                                    _code(wh, ACTIVATIONS, act, "act"), W_LAYOUTS[w_layout], 0)
-    _check(handle, load().muon_linear_grad_input(handle, ctypes.byref(a), _stream_on(stream, dev)))
+    pdy, lddy = k.matrix("dy", dy, (r, o), dt, "dy")
+    pw, ldw = k.matrix("w", w, w.shape, dt, "dy")
+    pdx, lddx = k.matrix("dx", dx, (r, i), dt, "dy")
+    pz, ldz = k.matrix("z", None if z8 is not None else z, (r, i), dt, "dy")
+    pv, ldv = k.matrix("act_out", act_out, (r, i), dt, "dy")
+    pa, lda = k.matrix("add", add, (r, i), dt, "dy")
+    a = muon_linear_grad_input_args(pdy, pw, pz, k.act8("z", z8, (r, i)), pa, pdx, pv, r, i, o, lddy, ldw, ldz, lda,
+                                    lddx, ldv, dc, ac, lay, 0)
+    _check(handle, load().muon_linear_grad_input(handle, a, k.stream(stream)))
 
 
 def muon_linear_grad_weight(handle: int, x, dy, dw, db=None, accumulate: bool = False, w_layout: str = "in_out",
                             stream=None) -> None:
     """dw = x^T dy (stored as the weight is) and db = dy's column sums; ``x`` is
     a tensor or an Act8, ``accumulate`` adds to dw and db."""
-    wh = "muon_linear_grad_weight"
-    k, n = _linear_sizes(wh, dw, w_layout)
-    if dy.dim() != 2:
-        raise ValueError(f"{wh}: dy must be 2-D")
-    r = int(dy.shape[0])
+    k = _Args("muon_linear_grad_weight", dy)
+    i, o, lay = _linear_sizes(k, dw, w_layout)
+    r = k.rows_cols("dy", dy)[0]
+    dt, dc, wc = dy.dtype, k.storage("dy", dy), k.storage("dw", dw)
     x8 = x if isinstance(x, Act8) else None
-    xt = None if x8 is not None else x
-    dev = _layer_tensors(wh, [("x", x, (r, k)), ("dy", dy, (r, n)), ("dw", dw, dw.shape), ("db", db, (n,))],
-                         [[("dy", dy), ("x", xt)], [("dw", dw)], [("db", db)]])
-    a = muon_linear_grad_weight_args(_ptr(xt), x8._c() if x8 is not None else _NO_ACT8, dy.data_ptr(), dw.data_ptr(),
-                                     _ptr(db), r, k, n, _ld2(xt) if xt is not None else 0, _ld2(dy), _ld2(dw),
-                                     _dtype_code(dy), _dtype_code(dw), _dtype_code(db) if db is not None else MUON_F32,
-                                     W_LAYOUTS[w_layout], int(bool(accumulate)), 0)
-    _check(handle, load().muon_linear_grad_weight(handle, ctypes.byref(a), _stream_on(stream, dev)))
+    pdy, lddy = k.matrix("dy", dy, (r, o), dt, "dy")
+    px, ldx = k.matrix("x", None if x8 is not None else x, (r, i), dt, "dy")
+    pdw, lddw = k.matrix("dw", dw, dw.shape, dw.dtype, "dw")
+    bc = MUON_F32 if db is None else k.storage("db", db)
+    a = muon_linear_grad_weight_args(px, k.act8("x", x8, (r, i)), pdy, pdw,
+                                     k.vector("db", db, o, db.dtype) if db is not None else None, r, i, o, ldx, lddy,
+                                     lddw, dc, wc, bc, lay, 1 if accumulate else 0, 0)
+    _check(handle, load().muon_linear_grad_weight(handle, a, k.stream(stream)))
 
 
 def muon_act_encode(handle: int, x, q: Act8, stream=None) -> None:
     """``q`` = the 8-bit checkpoint of x (2-D, bfloat16 or float32)."""
-    w = "muon_act_encode"
-    if x.dim() != 2:
-        raise ValueError(f"{w}: x must be 2-D")
-    dev = _layer_tensors(w, [("x", x, x.shape), ("q", q, x.shape)], [[("x", x)]])
-    c = q._c()
-    _check(handle, load().muon_act_encode(handle, x.data_ptr(), int(x.shape[0]), int(x.shape[1]), _ld2(x),
-                                          _dtype_code(x), ctypes.byref(c), _stream_on(stream, dev)))
+    k = _Args("muon_act_encode", x)
+    r, c = k.rows_cols("x", x)
+    dc = k.storage("x", x)
+    a = k.act8("q", q, x.shape)
+    _check(handle, load().muon_act_encode(handle, x.data_ptr(), r, c, _ld2(x), dc, a, k.stream(stream)))
 
 
 def muon_act_decode(handle: int, q: Act8, y, stream=None) -> None:
     """y (bfloat16 or float32) = what the checkpoint ``q`` stands for, exactly."""
-    w = "muon_act_decode"
-    if y.dim() != 2:
-        raise ValueError(f"{w}: y must be 2-D")
-    dev = _layer_tensors(w, [("y", y, y.shape), ("q", q, y.shape)], [[("y", y)]])
-    c = q._c()
-    _check(handle, load().muon_act_decode(handle, ctypes.byref(c), y.data_ptr(), int(y.shape[0]), int(y.shape[1]),
-                                          _ld2(y), _dtype_code(y), _stream_on(stream, dev)))
+    k = _Args("muon_act_decode", y)
+    r, c = k.rows_cols("y", y)
+    dc = k.storage("y", y)
+    a = k.act8("q", q, y.shape)
+    _check(handle, load().muon_act_decode(handle, a, y.data_ptr(), r, c, _ld2(y), dc, k.stream(stream)))
 
 
 def muon_read_norms(handle: int, n: int, stream=None) -> List[float]:

@@ -215,11 +215,15 @@ muon_status run_linear(HandleBase* h, LinArgs& a, hipStream_t stream) {
     a.splits = p.splits;
     a.tile = p.tile;
     void* ws = nullptr;
-    const size_t pb = (p.partial_bytes + 255) & ~size_t(255);
-    const muon_status st = workspace(h, pb + p.db_bytes, stream, &ws);
+    auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+    const size_t pb = up(p.partial_bytes), bb = up(p.db_bytes);
+    const muon_status st = workspace(h, pb + bb + p.decode_bytes, stream, &ws);
     if (st != MUON_OK) return st;
-    a.partial = static_cast<float*>(ws);
-    a.db_partial = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + pb) : nullptr;
+    char* base = static_cast<char*>(ws);
+    a.partial = reinterpret_cast<float*>(base);
+    a.db_partial = p.db_bytes ? reinterpret_cast<float*>(base + pb) : nullptr;
+    a.decoded = p.decode_ld ? base + pb + bb : nullptr;
+    a.decode_ld = p.decode_ld;
     const hipError_t e = launch_linear(a, stream);
     if (e != hipSuccess) return hip_fail(h, e, "linear launch");
     return MUON_OK;
@@ -385,6 +389,7 @@ muon_status muon_linear_forward(muon_handle* handle, const muon_linear_args* arg
     a.out_vec = rows_vec(p.y, p.ld_y, p.dtype);
     a.bias = p.bias;
     a.bias_dt = dt_code(p.bias_dtype);
+    a.bias_vec = aligned(p.bias, 16);
     a.add = p.residual;
     a.ld_add = p.ld_residual;
     a.add_vec = p.residual && rows_vec(p.residual, p.ld_residual, p.dtype);

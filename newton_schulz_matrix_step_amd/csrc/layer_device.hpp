@@ -115,11 +115,14 @@ __device__ __forceinline__ void act8_dec4(uint32_t w, float step, float* v) {
 constexpr float kGeluU = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 
-__device__ __forceinline__ float logistic(float u) {
-    return __builtin_amdgcn_rcpf(1.f + __expf(-u));
+// exp(-u(z)) as 2^x: x = -log2(e) u, its constants folded.
+constexpr float kGeluE1 = -2.302208198144325f;     // -2 sqrt(2 / pi) log2(e)
+constexpr float kGeluE3 = -0.10294323958002269f;   // and times 0.044715
+__device__ __forceinline__ float gelu_exp(float z) {
+    return __builtin_amdgcn_exp2f(z * fmaf(kGeluE3 * z, z, kGeluE1));
 }
 __device__ __forceinline__ float act_value(float z, int act) {
-    if (act == ACT_GELU) return z * logistic(kGeluU * z * fmaf(kGeluC * z, z, 1.f));
+    if (act == ACT_GELU) return z * __builtin_amdgcn_rcpf(1.f + gelu_exp(z));
     if (act == ACT_RELU_SQ) return z <= 0.f ? 0.f : z * z;   // a NaN stays one
     return z;
 }
@@ -129,7 +132,7 @@ __device__ __forceinline__ float act_value(float z, int act) {
 __device__ __forceinline__ void act_both(float z, int act, float& v, float& d) {
     if (act == ACT_GELU) {
         const float c = z < -9.f ? -9.f : (z > 9.f ? 9.f : z);   // a NaN stays one
-        const float e = __expf(-kGeluU * c * fmaf(kGeluC * c, c, 1.f));
+        const float e = gelu_exp(c);
         const float s = __builtin_amdgcn_rcpf(1.f + e);
         v = (z > 0.f ? z : c) * s;
         d = fmaf(c * s * (e * s), kGeluU * fmaf(3.f * kGeluC * c, c, 1.f), s);

@@ -110,7 +110,7 @@ struct LinArgs {
     int64_t ld_out;
     int32_t out_trans, out_dt, out_vec, accumulate;
     const void* bias;          // N, LIN_FWD
-    int32_t bias_dt;
+    int32_t bias_dt, bias_vec;
     const void* add;           // M x N: residual (LIN_FWD) or gradient to add (LIN_DX)
     int64_t ld_add;
     int32_t add_vec;
@@ -130,12 +130,15 @@ struct LinArgs {
     int32_t tile;              // tile edge: 128 or 256
     float* partial;
     float* db_partial;
+    void* decoded;             // A decoded from 8 bits, K rows of decode_ld bf16; 0: decoded by the product
+    int64_t decode_ld;
 };
 
 struct LinPlan {
     int tile = 128;
     int splits = 1;
-    size_t partial_bytes = 0, db_bytes = 0;
+    int64_t decode_ld = 0;
+    size_t partial_bytes = 0, db_bytes = 0, decode_bytes = 0;
 };
 LinPlan plan_linear(const LinArgs& a);
 hipError_t launch_linear(const LinArgs& a, hipStream_t s);

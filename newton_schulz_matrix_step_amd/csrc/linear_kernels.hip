@@ -9,6 +9,7 @@
 // v_mfma_f32_16x16x4_f32 for float32 tensors) with float32 sums, and every
 // result is rounded once, at its store.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "layer_device.hpp"
@@ -42,18 +43,22 @@ __device__ __forceinline__ i32x4_t buffer_at(const char* p, uint32_t bytes) {
 }
 
 #ifndef MUON_BUFFER_TO_LDS
+__device__ __forceinline__ uint32_t lds_base(const char* smem) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LDS_AS const char*)smem));
+}
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 // 16 bytes per lane from the buffer straight into LDS: lane L's bytes land at
-// lds + 16 L (lds wave-uniform); a lane whose offset lies past the buffer's end
-// stores zeros.  Nothing is returned in registers; completion counts in vmcnt.
-__device__ __forceinline__ void buffer_to_lds(i32x4_t buf, uint32_t voff, char* lds) {
-    const uint32_t a = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LDS_AS char*)lds)));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(a), "v"(voff), "s"(buf)
+// LDS address lds + 16 L (lds wave-uniform); a lane whose offset lies past the
+// buffer's end stores zeros.  Nothing is returned in registers; completion
+// counts in vmcnt.
+__device__ __forceinline__ void buffer_to_lds(i32x4_t buf, uint32_t voff, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(buf)
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
 #else
+#define lds_base MUON_LDS_BASE
 #define buffer_to_lds MUON_BUFFER_TO_LDS
 #endif
 
@@ -139,8 +144,8 @@ struct Loader {
         }
     }
 
-    // S_DMA: enqueue the stage at k0 into LDS at st
-    __device__ __forceinline__ void issue(int64_t k0, char* st) {
+    // S_DMA: enqueue the stage at k0 into LDS at address st
+    __device__ __forceinline__ void issue(int64_t k0, uint32_t st) {
         if constexpr (SRC == S_DMA) {
             if constexpr (KC) {
                 const i32x4_t buf = buffer_at(base + k0 * ES, kMaxRecords);
@@ -310,17 +315,22 @@ __device__ __forceinline__ void join_tiles(f32x4_t a, f32x4_t b, float (&v)[8]) 
 
 // 8 consecutive elements (r, c ..) of the output, nv of them inside (0: none).
 // SH: lane distance between the four lanes that share a group of 32 columns.
-template <int SH>
+// KIND: the product, or -1 to take it from the arguments.  FAST: all 8 elements
+// lie inside and every buffer of the epilogue allows vectors (see fast_epilogue).
+// DT: the tensors' type (a Num's dt), or -1 to take that from the arguments.
+template <int SH, int KIND, bool FAST, int DT>
 __device__ __forceinline__ void epilogue8(const LinArgs& a, int64_t r, int64_t c, int nv, float (&v)[8]) {
-    const int kind = a.kind;
+    const int kind = KIND >= 0 ? KIND : a.kind;
+    const int dt = DT >= 0 ? DT : a.dt, out_dt = kind == LIN_DW ? a.out_dt : dt;
+    if (FAST) nv = 8;
     if (kind == LIN_FWD) {
         if (a.bias) {
             float b[8];
-            load8(a.bias, c, a.bias_dt, false, nv, b);
+            load8(a.bias, c, a.bias_dt, FAST, nv, b);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += b[k];
         }
-        if (a.z && nv > 0) store8(a.z, r * a.ld_z + c, a.dt, a.z_vec, nv, v);
+        if (a.z && nv > 0) store8(a.z, r * a.ld_z + c, dt, FAST || a.z_vec, nv, v);
         if (a.z8.codes) {
             float m = 0.f;
 #pragma unroll
@@ -330,7 +340,7 @@ __device__ __forceinline__ void epilogue8(const LinArgs& a, int64_t r, int64_t c
             if (nv > 0) {
                 const uint32_t e = act8_exp(m);
                 GMEM int8_t* p = gm(a.z8.codes) + r * a.z8.ld + c;
-                if (a.z8.vec && nv >= 8) {
+                if (FAST || (a.z8.vec && nv >= 8)) {
                     u32x2_t w = {0u, 0u};
 #pragma unroll
                     for (int k = 0; k < 8; ++k) w[k >> 2] |= act8_code(v[k], e) << (8 * (k & 3));
@@ -344,20 +354,23 @@ __device__ __forceinline__ void epilogue8(const LinArgs& a, int64_t r, int64_t c
             }
         }
         if (nv <= 0) return;
-        if (a.act != ACT_NONE) {
+        if (a.act == ACT_GELU) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], a.act);
+            for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], ACT_GELU);
+        } else if (a.act == ACT_RELU_SQ) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], ACT_RELU_SQ);
         }
     } else if (kind == LIN_DX) {
         if (nv <= 0) return;
         if (a.z || a.z8.codes) {
             float z[8], h[8];
             if (a.z) {
-                load8(a.z, r * a.ld_z + c, a.dt, a.z_vec, nv, z);
+                load8(a.z, r * a.ld_z + c, dt, FAST || a.z_vec, nv, z);
             } else {
                 const float step = act8_step(gm(a.z8.exps)[r * a.z8.lde + c / kAct8Group]);
                 const GMEM int8_t* p = gm(a.z8.codes) + r * a.z8.ld + c;
-                if (a.z8.vec && nv >= 8) {
+                if (FAST || (a.z8.vec && nv >= 8)) {
                     const u32x2_t w = *reinterpret_cast<const GMEM u32x2_t*>(p);
                     act8_dec4(w[0], step, z);
                     act8_dec4(w[1], step, z + 4);
@@ -366,30 +379,40 @@ __device__ __forceinline__ void epilogue8(const LinArgs& a, int64_t r, int64_t c
                     for (int k = 0; k < 8; ++k) z[k] = k < nv ? float(p[k]) * step : 0.f;
                 }
             }
+            float d[8];
+            if (a.act == ACT_GELU) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float d;
-                act_both(z[k], a.act, h[k], d);
-                v[k] *= d;
+                for (int k = 0; k < 8; ++k) act_both(z[k], ACT_GELU, h[k], d[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) act_both(z[k], a.act, h[k], d[k]);
             }
-            if (a.act_out) store8(a.act_out, r * a.ld_act + c, a.dt, a.act_vec, nv, h);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= d[k];
+            if (a.act_out) store8(a.act_out, r * a.ld_act + c, dt, FAST || a.act_vec, nv, h);
         }
     } else {
         if (nv <= 0) return;
         if (a.accumulate) {
             float o[8];
-            load8(a.out, r * a.ld_out + c, a.out_dt, a.out_vec, nv, o);
+            load8(a.out, r * a.ld_out + c, out_dt, FAST || a.out_vec, nv, o);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += o[k];
         }
     }
-    if (a.add) {
+    if (kind != LIN_DW && a.add) {
         float b[8];
-        load8(a.add, r * a.ld_add + c, a.dt, a.add_vec, nv, b);
+        load8(a.add, r * a.ld_add + c, dt, FAST || a.add_vec, nv, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
-    store8(a.out, r * a.ld_out + c, a.out_dt, a.out_vec, nv, v);
+    store8(a.out, r * a.ld_out + c, out_dt, FAST || a.out_vec, nv, v);
+}
+
+// Every buffer that the epilogue touches allows vectors.
+__device__ __forceinline__ bool vector_epilogue(const LinArgs& a) {
+    return a.out_vec && (!a.bias || a.bias_vec) && (!a.add || a.add_vec) && (!a.z || a.z_vec) &&
+           (!a.z8.codes || a.z8.vec) && (!a.act_out || a.act_vec);
 }
 
 // Shape of the output as stored, and of the split sums (rows padded to whole groups).
@@ -404,21 +427,38 @@ __host__ __device__ inline OutShape out_shape(const LinArgs& a) {
     return o;
 }
 
-// 8 elements of this workgroup's tile: straight to the result, or to the sums
-// of its split.
-__device__ __forceinline__ void emit8(const LinArgs& a, const OutShape& o, int split, int64_t r, int64_t c,
-                                      float (&v)[8]) {
-    int64_t n = o.cols - c;
-    n = r < o.rows ? (n > 8 ? 8 : n) : 0;
-    if (a.splits > 1) {
-        if (n > 0) {   // the row's padding takes whole runs
-            GMEM float* p = gm(a.partial) + (int64_t(split) * o.rows + r) * o.ldp + c;
-            *reinterpret_cast<GMEM f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<GMEM f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
-        }
-        return;
+// 8 elements of a split's sums.
+__device__ __forceinline__ void put_partial(const LinArgs& a, const OutShape& o, int split, int64_t r, int64_t c,
+                                            const float (&v)[8]) {
+    if (r >= o.rows || c >= o.cols) return;   // a run that begins inside may end in the row's padding
+    GMEM float* p = gm(a.partial) + (int64_t(split) * o.rows + r) * o.ldp + c;
+    *reinterpret_cast<GMEM f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<GMEM f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+}
+
+// The output tile (ROWS x COLS at r0, c0, in the output's orientation) lies in
+// LDS as float32 rows: through the general epilogue, 8 elements a lane.  One
+// copy of its code, for tiles at the edges and buffers without vectors.
+__device__ __forceinline__ int stage_at(int cols, int r, int c) {   // float index of 4 elements; chunks XOR row
+    return r * cols + (((c >> 2) ^ (r & 15)) << 2);
+}
+template <int THREADS>
+__device__ __forceinline__ void staged_epilogue(const LinArgs& a, const OutShape& o, const float* stage, int rows,
+                                                int cols, int64_t r0, int64_t c0) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * cols / 8; i += THREADS) {
+        const int r = i / (cols / 8), c = i % (cols / 8) * 8;
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(stage + stage_at(cols, r, c));
+        const f32x4_t y = *reinterpret_cast<const f32x4_t*>(stage + stage_at(cols, r, c + 4));
+        float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        int64_t n = o.cols - (c0 + c);
+        n = r0 + r < o.rows ? (n > 8 ? 8 : n) : 0;
+        epilogue8<1, -1, false, -1>(a, r0 + r, c0 + c, n > 0 ? int(n) : 0, v);
     }
-    epilogue8<16>(a, r, c, n > 0 ? int(n) : 0, v);
+}
+__device__ __forceinline__ void stage_put(float* stage, int cols, int r, int c, const float (&v)[8]) {
+    *reinterpret_cast<f32x4_t*>(stage + stage_at(cols, r, c)) = f32x4_t{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4_t*>(stage + stage_at(cols, r, c + 4)) = f32x4_t{v[4], v[5], v[6], v[7]};
 }
 
 __device__ __forceinline__ void emit_db(const LinArgs& a, int split, int64_t n, float v) {
@@ -458,10 +498,11 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs& a, int edge) {
 // share a CU and one's epilogue overlaps the other's main loop).
 // TR: the accumulators hold runs along M (the output is stored transposed).
 // ---------------------------------------------------------------------------
-template <class T, bool AKC, bool BKC, int ASRC, int BSRC, bool TR>
+template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR>
 __global__ __launch_bounds__(256) void linear_tile_kernel(LinArgs a) {
     using N = Num<T>;
     __shared__ __align__(1024) char smem[4 * kOpBytes];
+    const uint32_t lds0 = lds_base(smem);
     const TileAt t = tile_at(a, 128);
     if (!t.in) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
@@ -487,11 +528,11 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinArgs a) {
         for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     // the column sums of B: a product with a row of ones, in the tiles of the first tile row
-    const bool sum_b = a.db != nullptr && t.tm == 0 && wr == 0;
+    const bool sum_b = !AKC && a.db != nullptr && t.tm == 0 && wr == 0;
 
     if (kb0 < kb1) {
-        la.issue(kb0 * N::BK, smem);
-        lb.issue(kb0 * N::BK, smem + kOpBytes);
+        la.issue(kb0 * N::BK, lds0);
+        lb.issue(kb0 * N::BK, lds0 + kOpBytes);
         la.fetch(kb0 * N::BK);
         lb.fetch(kb0 * N::BK);
         la.put(smem);
@@ -504,8 +545,9 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinArgs a) {
         __syncthreads();     // and every other wave's; the other stage is free
         const bool more = kb + 1 < kb1;
         if (more) {
-            la.issue((kb + 1) * N::BK, nxt);
-            lb.issue((kb + 1) * N::BK, nxt + kOpBytes);
+            const uint32_t at = lds0 + uint32_t(nxt - smem);
+            la.issue((kb + 1) * N::BK, at);
+            lb.issue((kb + 1) * N::BK, at + kOpBytes);
             la.fetch((kb + 1) * N::BK);
             lb.fetch((kb + 1) * N::BK);
         }
@@ -534,26 +576,326 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinArgs a) {
     }
 
     const OutShape o = out_shape(a);
-    const int64_t m0 = t.tm * 128 + wr, n0 = t.tn * 128 + wc;
     const int g = lane >> 4, i16 = lane & 15;
+    const int64_t r0 = (TR ? t.tn : t.tm) * 128, c0 = (TR ? t.tm : t.tn) * 128;
+    // f(row, column, values): runs of 8 of this wave's part of the output tile
+    auto runs = [&](auto&& f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            float v[8];
-            if constexpr (TR) {   // column n0 + 16 i + i16 of C, rows m0 + 32 p + 8 g ..
-                join_tiles(acc[2 * p][i], acc[2 * p + 1][i], v);
-                emit8(a, o, t.split, n0 + 16 * i + i16, m0 + 32 * p + 8 * g, v);
-            } else {
-                join_tiles(acc[i][2 * p], acc[i][2 * p + 1], v);
-                emit8(a, o, t.split, m0 + 16 * i + i16, n0 + 32 * p + 8 * g, v);
+            for (int p = 0; p < 2; ++p) {
+                float v[8];
+                if constexpr (TR) {
+                    join_tiles(acc[2 * p][i], acc[2 * p + 1][i], v);
+                    f(wc + 16 * i + i16, wr + 32 * p + 8 * g, v);
+                } else {
+                    join_tiles(acc[i][2 * p], acc[i][2 * p + 1], v);
+                    f(wr + 16 * i + i16, wc + 32 * p + 8 * g, v);
+                }
             }
-        }
+    };
+    if (a.splits > 1) {
+        runs([&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, r0 + r, c0 + c, v); });
+    } else if (KIND >= 0 && r0 + 128 <= o.rows && c0 + 128 <= o.cols && vector_epilogue(a)) {
+        runs([&](int r, int c, float(&v)[8]) { epilogue8<16, KIND, true, N::dt>(a, r0 + r, c0 + c, 8, v); });
+    } else {
+        float* stage = reinterpret_cast<float*>(smem);
+        __syncthreads();                 // every wave has read its last fragments
+        runs([&](int r, int c, float(&v)[8]) { stage_put(stage, 128, r, c, v); });
+        __syncthreads();
+        staged_epilogue<256>(a, o, stage, 128, 128, r0, c0);
+    }
     if (sum_b && i16 == 0) {   // every column of the product with ones is the same
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) emit_db(a, t.split, n0 + 16 * j + 4 * g + e, dbs[j][e]);
+            for (int e = 0; e < 4; ++e) emit_db(a, t.split, t.tn * 128 + wc + 16 * j + 4 * g + e, dbs[j][e]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles of bf16, one workgroup of 8 waves per CU.
+//
+// The tile is cut into halves of 128 rows (A0, A1) and columns (B0, B1); a wave
+// owns a 64 x 32 block of each of the four quadrants, so a k block of 64 is four
+// phases of 16 MFMAs:  A0 B0, A0 B1, A1 B1, A1 B0.  A phase has a load section
+// (fragments of the operand half that the phase needs new, and the global loads
+// of one half of the k block after next) and an MFMA section, each ended by a
+// barrier.  The two waves that share a SIMD run half a phase apart (waves 4-7
+// pass one barrier more at the start): one issues MFMAs while the other reads
+// LDS, so the matrix cores see no LDS latency and no wait at a barrier.
+//
+// LDS holds two k blocks (128 KB), each as four halves of 16 KB that are
+// refilled one by one as soon as they have been read: B0 is read in phase 3 of
+// the block before, A0 in phase 0, B1 in 1, A1 in 2, and the loads of the block
+// after next go out in phases 0 (B0), 1 (A0), 2 (B1) and 3 (A1), one phase
+// after the half's last read by either group of waves.  A half is needed 7
+// phases after its loads were issued; at the end of a load section everything
+// but the 6 halves issued last (2 loads a wave each) has landed.  Loads past the
+// end of k are issued too and read as zeros, which keeps that count.
+// ---------------------------------------------------------------------------
+constexpr int kPpThreads = 512;
+
+template <bool KC>
+struct HalfLoader {
+    const char* base;
+    int64_t ld, kend;
+    uint32_t voff[2][2];       // [half][1 KB block]
+    int wave, lane;
+
+    static constexpr int CPR = KC ? 8 : 16;
+    __device__ __forceinline__ int lrow(int q) const { return (wave * 2 + q) * (64 / CPR) + lane / CPR; }
+    __device__ __forceinline__ int lchunk(int q) const {
+        const int r = lrow(q), c = lane % CPR;
+        return KC ? c ^ (r & 7) : c ^ ks_swizzle<uint16_t>(r);
+    }
+    __device__ __forceinline__ void init(const void* p, int64_t ld_, int64_t ext, int64_t e0, int64_t kend_, int wave_,
+                                         int lane_) {
+        ld = ld_;
+        kend = kend_;
+        wave = wave_;
+        lane = lane_;
+        base = static_cast<const char*>(p) + (KC ? e0 * ld : e0) * 2;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int r = lrow(q), c = lchunk(q);
+                if (KC) voff[hf][q] = e0 + hf * 128 + r < ext ? uint32_t((hf * 128 + r) * ld * 2 + c * 16) : kFar;
+                else voff[hf][q] = e0 + hf * 128 + c * 8 < ext ? uint32_t(r * ld * 2 + hf * 256 + c * 16) : kFar;
+            }
+    }
+    __device__ __forceinline__ void issue(int hf, int64_t k0, uint32_t lds) const {
+        if (KC) {
+            const i32x4_t buf = buffer_at(base + k0 * 2, kMaxRecords);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                buffer_to_lds(buf, k0 + lchunk(q) * 8 < kend ? voff[hf][q] : kFar, lds + (wave * 2 + q) * 1024);
+        } else {
+            int64_t n = (kend - k0) * ld * 2;
+            n = n < 0 ? 0 : (n > int64_t(kMaxRecords) ? int64_t(kMaxRecords) : n);
+            const i32x4_t buf = buffer_at(base + k0 * ld * 2, uint32_t(n));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) buffer_to_lds(buf, voff[hf][q], lds + (wave * 2 + q) * 1024);
+        }
+    }
+};
+
+// Fragments of a half with few registers for addresses: one base per operand
+// (the lane's part of the address of the wave's first row or column), from
+// which every read differs by constants, some of them XORed (the swizzles only
+// flip address bits: rows and columns step by 16 within a wave's aligned part).
+// The base is made opaque at every use, so that the addresses are formed where
+// they are used (one xor a read, beside the other waves' MFMAs) instead of all
+// being kept in registers across the loop.
+template <bool KC>
+__device__ __forceinline__ uint32_t frag_base(int w0, int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    if constexpr (KC) return uint32_t((w0 + i) * 128 + ((g ^ (i & 7)) << 4));
+    const int k = 8 * g + (i >> 2), n = w0 + 4 * (i & 3);
+    return uint32_t(k * 256 + (((n >> 3) ^ ks_swizzle<uint16_t>(k)) << 4) + (n & 7) * 2);
+}
+template <bool KC>
+__device__ __forceinline__ bf16x8_t frag_at(const char* smem, uint32_t base, int rc, int s, int region) {
+    if constexpr (KC) {
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(smem + region + ((s ? base ^ 64u : base) + rc * 128));
+        return __builtin_bit_cast(bf16x8_t, w);
+    } else {
+        i16x4_t h[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const char* p = smem + region + ((base ^ uint32_t((rc / 8 * 16) ^ (hh * 128))) + hh * 1024 + s * 8192);
+            h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4_t*)(p));
+        }
+        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+}
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+__device__ __forceinline__ void mem_fence() { asm volatile("" ::: "memory"); }
+__device__ __forceinline__ void pp_barrier() {
+    mem_fence();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    mem_fence();
+}
+// End of a load section: its LDS reads are done, all but the last 12 loads have landed.
+template <int VM>
+__device__ __forceinline__ void pp_wait() {
+    mem_fence();
+    __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4) | (0 << 8));
+    pp_barrier();
+}
+
+template <bool AKC, bool BKC, int KIND, bool TR>
+__global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinArgs a) {
+    __shared__ __align__(1024) char smem[8 * kOpBytes];
+    const uint32_t lds0 = lds_base(smem);
+    const TileAt t = tile_at(a, 256);
+    if (!t.in) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int64_t nkb = (a.K + 63) / 64, kbs = (nkb + a.splits - 1) / a.splits;
+    const int64_t kb0 = t.split * kbs, kb1 = kb0 + kbs < nkb ? kb0 + kbs : nkb;
+    const int64_t kend = kb1 * 64 < a.K ? kb1 * 64 : a.K;
+    const int nk = int(kb1 - kb0);
+    const int64_t k00 = kb0 * 64;
+    HalfLoader<AKC> la;
+    HalfLoader<BKC> lb;
+    la.init(a.a, a.lda, a.M, t.tm * 256, kend, wave, lane);
+    lb.init(a.b, a.ldb, a.N, t.tn * 256, kend, wave, lane);
+    const int wr = (wave >> 2) * 64, wc = (wave & 3) * 32;
+    const bool sum_b = KIND == LIN_DW && a.db != nullptr && t.tm == 0 && wr == 0;
+
+    f32x4_t acc[2][2][4][2], dbs[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            dbs[x][y] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[x][y][i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+    bf16x8_t fa[2][4], fb[2][2][2];      // [s][i]; [set][s][j]
+
+    auto half_a = [&](int par, int hf) { return (par * 4 + hf) * kOpBytes; };
+    auto half_b = [&](int par, int hf) { return (par * 4 + 2 + hf) * kOpBytes; };
+    const uint32_t base_a = frag_base<AKC>(wr, lane), base_b = frag_base<BKC>(wc, lane);
+    auto read_a = [&](int par, int hf) {
+        const uint32_t b = opaque(base_a);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fa[s][i] = frag_at<AKC>(smem, b, 16 * i, s, half_a(par, hf));
+    };
+    auto read_b = [&](int par, int hf, auto set) {
+        constexpr int S = decltype(set)::value;
+        const uint32_t b = opaque(base_b);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) fb[S][s][j] = frag_at<BKC>(smem, b, 16 * j, s, half_b(par, hf));
+    };
+    auto mul = [&](auto hh, auto gg, auto set, auto sum) {
+        constexpr int H = decltype(hh)::value, G = decltype(gg)::value, S = decltype(set)::value;
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[H][G][i][j] = TR ? mma(fa[s][i], fb[S][s][j], acc[H][G][i][j])
+                                         : mma(fb[S][s][j], fa[s][i], acc[H][G][i][j]);
+        if constexpr (KIND == LIN_DW && decltype(sum)::value) {
+            if (sum_b) {
+                const bf16x8_t one = ones<bf16x8_t>();
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) dbs[G][j] = mma(fb[S][s][j], one, dbs[G][j]);
+            }
+        }
+        __builtin_amdgcn_s_setprio(0);
+        pp_barrier();
+    };
+    constexpr std::integral_constant<int, 0> c0_{};
+    constexpr std::integral_constant<int, 1> c1_{};
+    // one k block: PAR its LDS buffer, and the register set that holds its B0
+    auto block = [&](auto par, int kb) {
+        constexpr int P = decltype(par)::value;
+        constexpr std::integral_constant<int, P> s0{};
+        constexpr std::integral_constant<int, 1 - P> s1{};
+        const int64_t k2 = k00 + int64_t(kb + 2) * 64;
+        read_a(P, 0);
+        lb.issue(0, k2, lds0 + half_b(P, 0));
+        pp_wait<12>();
+        mul(c0_, c0_, s0, std::true_type{});
+        read_b(P, 1, s1);
+        la.issue(0, k2, lds0 + half_a(P, 0));
+        pp_wait<12>();
+        mul(c0_, c1_, s1, std::true_type{});
+        read_a(P, 1);
+        lb.issue(1, k2, lds0 + half_b(P, 1));
+        pp_wait<12>();
+        mul(c1_, c1_, s1, std::false_type{});
+        read_b(1 - P, 0, s1);            // the next block's B0
+        la.issue(1, k2, lds0 + half_a(P, 1));
+        pp_wait<12>();
+        mul(c1_, c0_, s0, std::false_type{});
+    };
+
+    if (nk > 0) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int64_t k = k00 + p * 64;
+            lb.issue(0, k, lds0 + half_b(p, 0));
+            la.issue(0, k, lds0 + half_a(p, 0));
+            lb.issue(1, k, lds0 + half_b(p, 1));
+            la.issue(1, k, lds0 + half_a(p, 1));
+        }
+        pp_wait<14>();                   // B0 of the first block
+        read_b(0, 0, c0_);
+        pp_wait<12>();                   // and A0
+        if (wave >= 4) pp_barrier();     // half a phase behind from here on
+        for (int kb = 0; kb < nk; kb += 2) {
+            block(c0_, kb);
+            if (kb + 1 < nk) block(c1_, kb + 1);
+        }
+        if (wave < 4) pp_barrier();
+        vm_wait<0>();                    // no load may land after the workgroup's LDS is given away
+    }
+
+    const OutShape o = out_shape(a);
+    const int g = lane >> 4, i16 = lane & 15;
+    const int64_t r0 = (TR ? t.tn : t.tm) * 256, c0 = (TR ? t.tm : t.tn) * 256;
+    // f(row, column, values): runs of 8 of this wave's part of half h (128 rows) of the output tile
+    auto runs = [&](auto hh, auto&& f) {
+        constexpr int H = decltype(hh)::value;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+                if constexpr (TR) {      // i: column tile i & 1, row pair i >> 1
+                    join_tiles(acc[y][H][2 * (i >> 1)][i & 1], acc[y][H][2 * (i >> 1) + 1][i & 1], v);
+                    f(wc + 16 * (i & 1) + i16, y * 128 + wr + 32 * (i >> 1) + 8 * g, v);
+                } else {
+                    join_tiles(acc[H][y][i][0], acc[H][y][i][1], v);
+                    f(wr + 16 * i + i16, y * 128 + wc + 8 * g, v);
+                }
+            }
+    };
+    const bool fast = r0 + 256 <= o.rows && c0 + 256 <= o.cols && vector_epilogue(a);
+    auto half = [&](auto hh) {
+        const int64_t rh = r0 + 128 * decltype(hh)::value;
+        if (a.splits > 1) {
+            runs(hh, [&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, rh + r, c0 + c, v); });
+        } else if (fast) {
+            runs(hh, [&](int r, int c, float(&v)[8]) { epilogue8<16, KIND, true, 0>(a, rh + r, c0 + c, 8, v); });
+        } else {
+            float* stage = reinterpret_cast<float*>(smem);
+            __syncthreads();
+            runs(hh, [&](int r, int c, float(&v)[8]) { stage_put(stage, 256, r, c, v); });
+            __syncthreads();
+            staged_epilogue<kPpThreads>(a, o, stage, 128, 256, rh, c0);
+        }
+    };
+    half(c0_);
+    half(c1_);
+    if (sum_b && i16 == 0) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    emit_db(a, t.split, t.tn * 256 + y * 128 + wc + 16 * j + 4 * g + e, dbs[y][j][e]);
     }
 }
 
@@ -592,72 +934,132 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int64_t out
             }
         }
     }
-    epilogue8<1>(a, r, c, n > 0 ? int(n) : 0, v);
+    epilogue8<1, -1, false, -1>(a, r, c, n > 0 ? int(n) : 0, v);
 }
 
-template <class T, bool AKC, bool BKC, int ASRC, int BSRC, bool TR>
+template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR>
 hipError_t launch_tile(const LinArgs& a, hipStream_t s) {
     const int64_t nm = (a.M + 127) / 128, nn = (a.N + 127) / 128, all = nm * nn * a.splits;
-    hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, TR>), dim3(unsigned((all + 7) / 8 * 8)), dim3(256),
-                       0, s, a);
+    hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, KIND, TR>), dim3(unsigned((all + 7) / 8 * 8)),
+                       dim3(256), 0, s, a);
     return hipGetLastError();
+}
+template <bool AKC, bool BKC, int KIND, bool TR>
+hipError_t launch_pp(const LinArgs& a, hipStream_t s) {
+    const int64_t nm = (a.M + 255) / 256, nn = (a.N + 255) / 256, all = nm * nn * a.splits;
+    hipLaunchKernelGGL((linear_pp_kernel<AKC, BKC, KIND, TR>), dim3(unsigned((all + 7) / 8 * 8)), dim3(kPpThreads), 0, s,
+                       a);
+    return hipGetLastError();
+}
+
+hipError_t launch_256(const LinArgs& a, hipStream_t s) {
+    if (a.kind == LIN_FWD)
+        return a.b_kc ? launch_pp<true, true, LIN_FWD, false>(a, s) : launch_pp<true, false, LIN_FWD, false>(a, s);
+    if (a.kind == LIN_DX)
+        return a.b_kc ? launch_pp<true, true, LIN_DX, false>(a, s) : launch_pp<true, false, LIN_DX, false>(a, s);
+    return a.out_trans ? launch_pp<false, false, LIN_DW, true>(a, s) : launch_pp<false, false, LIN_DW, false>(a, s);
+}
+
+// x W or dy W^T: B by rows (KC) or by columns of k; element-wise loads for both
+// operands where either needs them.
+template <class T, bool BKC>
+hipError_t launch_rows(const LinArgs& a, hipStream_t s) {
+    if (!a.a_dma || !a.b_dma) return launch_tile<T, true, BKC, S_ANY, S_ANY, -1, false>(a, s);
+    return a.kind == LIN_FWD ? launch_tile<T, true, BKC, S_DMA, S_DMA, LIN_FWD, false>(a, s)
+                             : launch_tile<T, true, BKC, S_DMA, S_DMA, LIN_DX, false>(a, s);
+}
+template <class T, bool TR>
+hipError_t launch_dw(const LinArgs& a, hipStream_t s) {
+    if (a.a_exps)
+        return a.b_dma ? launch_tile<T, false, false, S_ACT8, S_DMA, LIN_DW, TR>(a, s)
+                       : launch_tile<T, false, false, S_ACT8, S_ANY, -1, TR>(a, s);
+    return a.a_dma && a.b_dma ? launch_tile<T, false, false, S_DMA, S_DMA, LIN_DW, TR>(a, s)
+                              : launch_tile<T, false, false, S_ANY, S_ANY, -1, TR>(a, s);
 }
 
 template <class T>
 hipError_t launch_typed(const LinArgs& a, hipStream_t s) {
-    // element-wise loads for both operands where either needs them
-    const bool dma = a.a_dma && a.b_dma;
-    if (a.kind != LIN_DW) {
-        if (a.b_kc)
-            return dma ? launch_tile<T, true, true, S_DMA, S_DMA, false>(a, s)
-                       : launch_tile<T, true, true, S_ANY, S_ANY, false>(a, s);
-        return dma ? launch_tile<T, true, false, S_DMA, S_DMA, false>(a, s)
-                   : launch_tile<T, true, false, S_ANY, S_ANY, false>(a, s);
-    }
-    if (a.a_exps) {
-        if (a.out_trans)
-            return a.b_dma ? launch_tile<T, false, false, S_ACT8, S_DMA, true>(a, s)
-                           : launch_tile<T, false, false, S_ACT8, S_ANY, true>(a, s);
-        return a.b_dma ? launch_tile<T, false, false, S_ACT8, S_DMA, false>(a, s)
-                       : launch_tile<T, false, false, S_ACT8, S_ANY, false>(a, s);
-    }
-    if (a.out_trans)
-        return dma ? launch_tile<T, false, false, S_DMA, S_DMA, true>(a, s)
-                   : launch_tile<T, false, false, S_ANY, S_ANY, true>(a, s);
-    return dma ? launch_tile<T, false, false, S_DMA, S_DMA, false>(a, s)
-               : launch_tile<T, false, false, S_ANY, S_ANY, false>(a, s);
+    if (a.kind == LIN_DW) return a.out_trans ? launch_dw<T, true>(a, s) : launch_dw<T, false>(a, s);
+    return a.b_kc ? launch_rows<T, true>(a, s) : launch_rows<T, false>(a, s);
 }
 
 }  // namespace
 
+// Tile edge and split of a product: the cheapest by a model of its time in us.
+// A wave of 128-wide tiles (two workgroups a CU) takes about 4 + 1.05 per k
+// block of 64, and less while each CU holds one workgroup; a wave of 256-wide
+// ones (one a CU) about 10 + 1.3 (1.25 where both operands are row-contiguous)
+// for twice the output.  Measured, bf16: 8192 x 1024 -> 4096 88 us on 128-wide
+// tiles, 74 on 256-wide ones; 4096 x 14336 -> 4096 440 and 374 (429 and 315
+// row-contiguous); 2048 x 2048 -> 1408, whose 48 wide tiles leave most CUs idle,
+// 28 and 52.  A split adds the second kernel's launch and its sums' traffic.
+// An 8-bit operand is decoded by the 128-wide kernel itself, which more than
+// doubles its time per k block, or by a pass of its own into the workspace
+// (8192 tokens, 1024 x 4096, 128-wide: 215 us fused, 95 + 7 in two passes).
 LinPlan plan_linear(const LinArgs& a) {
-    LinPlan p;
-    p.tile = 128;
-    const int64_t tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-    const int64_t bk = a.dt == 0 ? 64 : 32, nkb = (a.K + bk - 1) / bk;
-    // two workgroups a CU; a split keeps at least 4 k blocks
-    int64_t s = 1;
-    if (tiles < 512) {
-        s = 512 / tiles;
-        s = s < nkb / 4 ? s : nkb / 4;
-        s = s < 1 ? 1 : (s > 64 ? 64 : s);
-        if (s > 1) {   // no empty split
+    LinPlan best;
+    double best_us = 1e30;
+    const OutShape o = out_shape(a);
+    for (int decode = 0; decode <= (a.a_exps && a.dt == 0 ? 1 : 0); ++decode) {
+    const bool a_dma = decode ? true : a.a_dma != 0, fused8 = a.a_exps && !decode;
+    const bool wide_ok = a.dt == 0 && a_dma && a.b_dma;
+    const int64_t nkb = (a.K + (a.dt == 0 ? 64 : 32) - 1) / (a.dt == 0 ? 64 : 32);
+    for (int tile : {128, 256}) {
+        if (tile == 256 && !wide_ok) continue;
+        const int64_t tiles = ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile);
+        const int64_t slots = tile == 256 ? 256 : 512;
+        // a split keeps at least 4 k blocks and at most fills the slots once
+        int64_t most = std::min<int64_t>(std::min<int64_t>(nkb / 4, slots / tiles), 64);
+        for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
             const int64_t per = (nkb + s - 1) / s;
-            s = (nkb + per - 1) / per;
+            if (s > 1 && (nkb + per - 1) / per != s) continue;   // it would leave a split empty
+            const int64_t wgs = tiles * s;
+            double us;
+            if (tile == 256) us = double((wgs + 255) / 256) * (10 + (a.a_kc && a.b_kc ? 1.25 : 1.35) * double(per));
+            else us = double((wgs + 511) / 512) * (4 + (wgs <= 256 ? 0.75 : 1.05) * (a.dt == 0 ? 1.0 : 2.5) *
+                                                               (fused8 ? 2.3 : 1.0) * double(per));
+            if (decode) us += 2 + double(a.K) * double(a.M) * 3 / 4.5e6;
+            if (s > 1) us += 4 + double(s) * double(o.rows) * double(o.ldp) * 8 / 4.5e6;
+            if (us < best_us) {
+                best_us = us;
+                best.tile = tile;
+                best.splits = int(s);
+                best.decode_ld = decode ? (a.M + 7) / 8 * 8 : 0;
+            }
         }
     }
-    p.splits = int(s);
-    if (s > 1) {
-        const OutShape o = out_shape(a);
-        p.partial_bytes = size_t(s) * size_t(o.rows) * size_t(o.ldp) * 4;
-        p.db_bytes = a.db ? size_t(s) * size_t(a.N) * 4 : 0;
     }
-    return p;
+    best.decode_bytes = size_t(best.decode_ld) * size_t(a.K) * 2;
+    if (best.splits > 1) {
+        best.partial_bytes = size_t(best.splits) * size_t(o.rows) * size_t(o.ldp) * 4;
+        best.db_bytes = a.db ? size_t(best.splits) * size_t(a.N) * 4 : 0;
+    }
+    return best;
 }
 
-hipError_t launch_linear(const LinArgs& a, hipStream_t s) {
+hipError_t launch_linear(const LinArgs& args, hipStream_t s) {
+    LinArgs a = args;
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
-    hipError_t e = a.dt == 0 ? launch_typed<uint16_t>(a, s) : launch_typed<float>(a, s);
+    if (a.decode_ld) {   // the 8-bit operand as bf16 rows in the workspace
+        Act8Args q;
+        q.x = nullptr;
+        q.y = a.decoded;
+        q.q = Act8View{static_cast<int8_t*>(const_cast<void*>(a.a)), const_cast<uint8_t*>(a.a_exps), a.lda, a.lda_exps,
+                       a.a8_vec};
+        q.rows = a.K;
+        q.ld = a.decode_ld;
+        q.cols = int32_t(a.M);
+        q.dt = 0;
+        q.vec = a.a8_vec;
+        const hipError_t d = launch_act8_decode(q, s);
+        if (d != hipSuccess) return d;
+        a.a = a.decoded;
+        a.lda = a.decode_ld;
+        a.a_exps = nullptr;
+        a.a_dma = 1;
+    }
+    hipError_t e = a.tile == 256 ? launch_256(a, s)
+                                 : (a.dt == 0 ? launch_typed<uint16_t>(a, s) : launch_typed<float>(a, s));
     if (e != hipSuccess || a.splits <= 1) return e;
     const OutShape o = out_shape(a);
     const int64_t ob = (o.rows * (o.ldp / 8) + 255) / 256, db = a.db ? (a.N + 255) / 256 : 0;

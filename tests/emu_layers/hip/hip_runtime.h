@@ -23,8 +23,8 @@ inline void emu_launch2(const char* name, F f, dim3 g, dim3 b, A... a) {
 #define hipLaunchKernelGGL(K, G, B, SH, ST, ...) emu_launch2(#K, K, G, B, __VA_ARGS__)
 
 inline uint32_t __float_as_uint(float f) { uint32_t u; std::memcpy(&u, &f, 4); return u; }
-inline float emu_exp(float x) { return std::exp(x); }
-#define __expf emu_exp
+inline float emu_exp2(float x) { return std::exp2(x); }
+#define __builtin_amdgcn_exp2f emu_exp2
 #define __builtin_amdgcn_rcpf(x) (1.f / (x))
 typedef unsigned emu_u2 __attribute__((ext_vector_type(2)));
 #define __builtin_amdgcn_permlane32_swap(a, b, x, y) (emu_u2{(a), (b)})
@@ -34,9 +34,14 @@ typedef unsigned emu_u2 __attribute__((ext_vector_type(2)));
 #define __builtin_amdgcn_sched_barrier(x) ((void)0)
 
 // raw buffer: words 0-1 the base, word 2 the size in bytes; a lane past it stores zeros
+inline char* emu_lds;   // the running kernel's LDS: its addresses count from there
+inline uint32_t emu_lds_base(char* smem) {
+    emu_lds = smem;
+    return 0;
+}
 template <class V>
-inline void emu_buffer_to_lds(V buf, uint32_t voff, char* lds) {
-    char* dst = lds + (threadIdx.x & 63) * 16;
+inline void emu_buffer_to_lds(V buf, uint32_t voff, uint32_t lds) {
+    char* dst = emu_lds + lds + (threadIdx.x & 63) * 16;
     if (voff >= uint32_t(buf[2])) {
         std::memset(dst, 0, 16);
         return;
@@ -44,4 +49,5 @@ inline void emu_buffer_to_lds(V buf, uint32_t voff, char* lds) {
     const uint64_t base = uint64_t(uint32_t(buf[0])) | (uint64_t(uint32_t(buf[1])) << 32);
     std::memcpy(dst, reinterpret_cast<const char*>(base) + voff, 16);
 }
+#define MUON_LDS_BASE emu_lds_base
 #define MUON_BUFFER_TO_LDS emu_buffer_to_lds
