@@ -214,6 +214,7 @@ muon_status run_linear(HandleBase* h, LinArgs& a, hipStream_t stream) {
     const LinPlan p = plan_linear(a);
     a.splits = p.splits;
     a.tile = p.tile;
+    a.deep = p.deep;
     void* ws = nullptr;
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
     const size_t pb = up(p.partial_bytes), bb = up(p.db_bytes);

@@ -128,6 +128,7 @@ struct LinArgs {
     // [splits][N] of the column sums) and a second kernel joins them
     int32_t splits;
     int32_t tile;              // tile edge: 128 or 256
+    int32_t deep;              // 128-wide tiles: four LDS stages, one workgroup a CU
     float* partial;
     float* db_partial;
     void* decoded;             // A decoded from 8 bits, K rows of decode_ld bf16; 0: decoded by the product
@@ -137,6 +138,7 @@ struct LinArgs {
 struct LinPlan {
     int tile = 128;
     int splits = 1;
+    bool deep = false;
     int64_t decode_ld = 0;
     size_t partial_bytes = 0, db_bytes = 0, decode_bytes = 0;
 };

@@ -10,6 +10,7 @@
 // result is rounded once, at its store.
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "layer_device.hpp"
@@ -84,44 +85,49 @@ struct Num<float> {
 // S_ACT8 8-bit codes, decoded on their way through registers.
 enum Src { S_DMA, S_ANY, S_ACT8 };
 
-// One stage of one operand is 16 KB of LDS for a 128-wide tile.  Row-contiguous
-// operands (KC) lie as [row][8 chunks of 16 bytes along k], chunk XOR row & 7;
-// k-strided ones as [k][128 elements] with their own chunk swizzle.  Both feed
-// the fragment reads below without bank conflicts.
+// One stage of one operand is 128 bytes of LDS per tile row: 16 KB for a
+// 128-wide tile.  Row-contiguous operands (KC) lie as [row][8 chunks of 16 bytes
+// along k], chunk XOR row & 7; k-strided ones as [k][W elements] (W the tile
+// edge) with their own chunk swizzle.  Both feed the fragment reads below
+// without bank conflicts.
 constexpr int kOpBytes = 16384;
 
 // bf16 [k][128]: a ds_read_b64_tr_b16 group of 16 lanes reads 4 k rows x 32
 // bytes (bits 1-2 spread them over a 128-byte window, bit 3 moves the
-// neighbouring group to the other half); float32 [k][128]: the four lane groups
-// read rows 4 apart, which bits 2-3 put on different 64-byte windows.
-template <class T>
+// neighbouring group to the other half); [k][64]: two of the four rows share a
+// 256-byte window's half, so bit 1 goes by k >> 1, and bit 2 moves the
+// neighbouring group.  float32 [k][W]: the four lane groups read rows 4 apart,
+// which bits 2-3 put on different 64-byte windows.
+template <class T, int W>
 __device__ __forceinline__ int ks_swizzle(int k) {
-    if constexpr (Num<T>::dt == 0) return ((2 * k) & 6) | ((((k >> 3) ^ (k >> 2)) & 1) << 3);
-    else return ((k >> 2) & 3) << 2;
+    if constexpr (Num<T>::dt == 1) return ((k >> 2) & 3) << 2;
+    else if constexpr (W == 64) return (k & 2) | ((k >> 1) & 4);
+    else return ((2 * k) & 6) | ((((k >> 3) ^ (k >> 2)) & 1) << 3);
 }
 
-// The operand's rows (KC) or columns (KS) [e0, e0 + 128) of the tile, `ext`
-// existing in all; k runs to kend.
-template <class T, bool KC, int SRC>
+// The operand's rows (KC) or columns (KS) [e0, e0 + W) of the tile, `ext`
+// existing in all; k runs to kend.  Four waves load it.
+template <class T, bool KC, int SRC, int W>
 struct Loader {
     using N = Num<T>;
     static constexpr int ES = sizeof(T);
-    static constexpr int CPR = KC ? 8 : 128 * ES / 16;   // chunks of an LDS row
+    static constexpr int NQ = W / 32;                    // 1 KB blocks a wave loads of a stage
+    static constexpr int CPR = KC ? 8 : W * ES / 16;     // chunks of an LDS row
     static constexpr int RPB = 64 / CPR;                 // LDS rows of 1 KB
     const char* base;
     int64_t ld, ext, kend, e0;
     const uint8_t* exps;
     int64_t lde;
     bool vec8;
-    uint32_t voff[4];
-    u32x4_t reg[SRC == S_DMA ? 1 : 4];
+    uint32_t voff[NQ];
+    u32x4_t reg[SRC == S_DMA ? 1 : NQ];
     int wave, lane;
 
     // LDS row and logical chunk of this lane's part of 1 KB block q
-    __device__ __forceinline__ int lrow(int q) const { return (wave * 4 + q) * RPB + lane / CPR; }
+    __device__ __forceinline__ int lrow(int q) const { return (wave * NQ + q) * RPB + lane / CPR; }
     __device__ __forceinline__ int lchunk(int q) const {
         const int r = lrow(q), c = lane % CPR;
-        return KC ? c ^ (r & 7) : c ^ ks_swizzle<T>(r);
+        return KC ? c ^ (r & 7) : c ^ ks_swizzle<T, W>(r);
     }
 
     __device__ __forceinline__ void init(const void* p, int64_t ld_, int64_t ext_, int64_t e0_, int64_t kend_, int wave_,
@@ -136,7 +142,7 @@ struct Loader {
         if constexpr (SRC == S_DMA) {
             base += (KC ? e0 * ld : e0) * ES;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < NQ; ++q) {
                 const int r = lrow(q), c = lchunk(q);
                 const bool in = KC ? e0 + r < ext : e0 + c * N::EPC < ext;
                 voff[q] = in ? uint32_t(r * ld * ES + c * 16) : kFar;
@@ -150,16 +156,16 @@ struct Loader {
             if constexpr (KC) {
                 const i32x4_t buf = buffer_at(base + k0 * ES, kMaxRecords);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < NQ; ++q) {
                     const bool in = k0 + lchunk(q) * N::EPC < kend;   // a whole chunk is in or out
-                    buffer_to_lds(buf, in ? voff[q] : kFar, st + (wave * 4 + q) * 1024);
+                    buffer_to_lds(buf, in ? voff[q] : kFar, st + (wave * NQ + q) * 1024);
                 }
             } else {
                 int64_t n = (kend - k0) * ld * ES;   // rows past kend lie past the buffer
                 n = n < 0 ? 0 : (n > int64_t(kMaxRecords) ? int64_t(kMaxRecords) : n);
                 const i32x4_t buf = buffer_at(base + k0 * ld * ES, uint32_t(n));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) buffer_to_lds(buf, voff[q], st + (wave * 4 + q) * 1024);
+                for (int q = 0; q < NQ; ++q) buffer_to_lds(buf, voff[q], st + (wave * NQ + q) * 1024);
             }
         }
     }
@@ -169,7 +175,7 @@ struct Loader {
         if constexpr (SRC == S_ANY) {
             const GMEM T* p = gm(reinterpret_cast<const T*>(base));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < NQ; ++q) {
                 const int64_t r = KC ? e0 + lrow(q) : k0 + lrow(q);
                 const int64_t c = (KC ? k0 : e0) + lchunk(q) * N::EPC;
                 const int64_t rn = KC ? ext : kend, cn = KC ? kend : ext;
@@ -187,7 +193,7 @@ struct Loader {
             static_assert(!KC, "checkpoints are stored by rows of k here");
             const GMEM int8_t* p = gm(reinterpret_cast<const int8_t*>(base));
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < NQ; ++q) {
                 const int64_t k = k0 + lrow(q);
                 const int64_t c = e0 + lchunk(q) * N::EPC;
                 u32x4_t r = {0u, 0u, 0u, 0u};   // codes in [0..1], the exponent byte in [2]
@@ -216,10 +222,10 @@ struct Loader {
     __device__ __forceinline__ void put(char* st) {
         if constexpr (SRC == S_ANY) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) *reinterpret_cast<u32x4_t*>(st + (wave * 4 + q) * 1024 + lane * 16) = reg[q];
+            for (int q = 0; q < NQ; ++q) *reinterpret_cast<u32x4_t*>(st + (wave * NQ + q) * 1024 + lane * 16) = reg[q];
         } else if constexpr (SRC == S_ACT8) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < NQ; ++q) {
                 const float step = act8_step(reg[q][2]);
                 float v[8];
                 act8_dec4(reg[q][0], step, v);
@@ -233,7 +239,7 @@ struct Loader {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[e]);
                 }
-                *reinterpret_cast<u32x4_t*>(st + (wave * 4 + q) * 1024 + lane * 16) = w;
+                *reinterpret_cast<u32x4_t*>(st + (wave * NQ + q) * 1024 + lane * 16) = w;
             }
         }
     }
@@ -245,7 +251,7 @@ struct Loader {
 // for each of four MFMAs; both operands use the same k for the same lane group
 // and e, which is all a sum over k asks for.
 // ---------------------------------------------------------------------------
-template <class T, bool KC>
+template <class T, bool KC, int W>
 __device__ __forceinline__ auto frag(const char* lds, int rc, int s, int lane) {
     const int g = lane >> 4, i = lane & 15;
     if constexpr (KC) {
@@ -259,7 +265,7 @@ __device__ __forceinline__ auto frag(const char* lds, int rc, int s, int lane) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
             const int k = 32 * s + 8 * g + 4 * hh + (i >> 2);
-            const char* p = lds + k * 256 + (((n >> 3) ^ ks_swizzle<T>(k)) << 4) + (n & 7) * 2;
+            const char* p = lds + k * (W * 2) + (((n >> 3) ^ ks_swizzle<T, W>(k)) << 4) + (n & 7) * 2;
             h[hh] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS i16x4_t*)(p));
         }
         return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
@@ -269,7 +275,7 @@ __device__ __forceinline__ auto frag(const char* lds, int rc, int s, int lane) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int k = 16 * s + 4 * g + e;
-            v[e] = *reinterpret_cast<const float*>(lds + k * 512 + (((n >> 2) ^ ks_swizzle<T>(k)) << 4) + (n & 3) * 4);
+            v[e] = *reinterpret_cast<const float*>(lds + k * (W * 4) + (((n >> 2) ^ ks_swizzle<T, W>(k)) << 4) + (n & 3) * 4);
         }
         return v;
     }
@@ -494,96 +500,139 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs& a, int edge) {
 }
 
 // ---------------------------------------------------------------------------
-// 128 x 128 tiles: 4 waves of 64 x 64, two LDS stages (64 KB, so two workgroups
-// share a CU and one's epilogue overlaps the other's main loop).
+// W x W tiles: 4 waves of W/2 x W/2 and a ring of NST LDS stages.  With W = 128
+// and two stages (64 KB) two workgroups share a CU and one's epilogue and waits
+// overlap the other's MFMAs.  Where there are no more workgroups than CUs, four
+// stages (128 KB) let the fragments be read half a block ahead (below): 2048 x
+// 2048 -> 1408 28 -> 23 us.  W = 64 with four stages (64 KB) serves outputs of
+// few tiles.
 // TR: the accumulators hold runs along M (the output is stored transposed).
 // ---------------------------------------------------------------------------
-template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR>
-__global__ __launch_bounds__(256) void linear_tile_kernel(LinArgs a) {
+template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR, int W, int NST>
+__global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
     using N = Num<T>;
-    __shared__ __align__(1024) char smem[4 * kOpBytes];
+    constexpr int OPB = W * 128;         // LDS bytes of an operand's stage
+    constexpr int TI = W / 32;           // 16-wide fragments of a wave's edge
+    __shared__ __align__(1024) char smem[NST * 2 * OPB];
+    static_assert(NST == 2 || (ASRC == S_DMA && BSRC == S_DMA), "registers stage one block ahead");
     const uint32_t lds0 = lds_base(smem);
-    const TileAt t = tile_at(a, 128);
+    const TileAt t = tile_at(a, W);
     if (!t.in) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int64_t nkb = (a.K + N::BK - 1) / N::BK, kbs = (nkb + a.splits - 1) / a.splits;
     const int64_t kb0 = t.split * kbs, kb1 = kb0 + kbs < nkb ? kb0 + kbs : nkb;
     const int64_t kend = kb1 * N::BK < a.K ? kb1 * N::BK : a.K;
-    Loader<T, AKC, ASRC> la;
-    Loader<T, BKC, BSRC> lb;
-    la.init(a.a, a.lda, a.M, t.tm * 128, kend, wave, lane);
-    lb.init(a.b, a.ldb, a.N, t.tn * 128, kend, wave, lane);
+    Loader<T, AKC, ASRC, W> la;
+    Loader<T, BKC, BSRC, W> lb;
+    la.init(a.a, a.lda, a.M, t.tm * W, kend, wave, lane);
+    lb.init(a.b, a.ldb, a.N, t.tn * W, kend, wave, lane);
     if constexpr (ASRC == S_ACT8) {
         la.exps = a.a_exps;
         la.lde = a.lda_exps;
         la.vec8 = a.a8_vec != 0;
     }
-    const int wr = (wave >> 1) * 64, wc = (wave & 1) * 64;
-    f32x4_t acc[4][4];
-    f32x4_t dbs[4];
+    const int wr = (wave >> 1) * (W / 2), wc = (wave & 1) * (W / 2);
+    f32x4_t acc[TI][TI];
+    f32x4_t dbs[TI];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < TI; ++i) {
         dbs[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < TI; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
     // the column sums of B: a product with a row of ones, in the tiles of the first tile row
     const bool sum_b = !AKC && a.db != nullptr && t.tm == 0 && wr == 0;
 
-    if (kb0 < kb1) {
-        la.issue(kb0 * N::BK, lds0);
-        lb.issue(kb0 * N::BK, lds0 + kOpBytes);
-        la.fetch(kb0 * N::BK);
-        lb.fetch(kb0 * N::BK);
-        la.put(smem);
-        lb.put(smem + kOpBytes);
-    }
-    for (int64_t kb = kb0; kb < kb1; ++kb) {
-        char* cur = smem + ((kb - kb0) & 1) * 2 * kOpBytes;
-        char* nxt = smem + ((kb - kb0 + 1) & 1) * 2 * kOpBytes;
-        vm_wait<0>();        // this wave's part of the stage has landed
-        __syncthreads();     // and every other wave's; the other stage is free
-        const bool more = kb + 1 < kb1;
-        if (more) {
-            const uint32_t at = lds0 + uint32_t(nxt - smem);
-            la.issue((kb + 1) * N::BK, at);
-            lb.issue((kb + 1) * N::BK, at + kOpBytes);
-            la.fetch((kb + 1) * N::BK);
-            lb.fetch((kb + 1) * N::BK);
+    using F = decltype(frag<T, AKC, W>(smem, 0, 0, 0));
+    auto read = [&](const char* st, int s, F(&fa)[TI], F(&fb)[TI]) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i) fa[i] = frag<T, AKC, W>(st, wr + 16 * i, s, lane);
+#pragma unroll
+        for (int j = 0; j < TI; ++j) fb[j] = frag<T, BKC, W>(st + OPB, wc + 16 * j, s, lane);
+    };
+    auto mul = [&](const F(&fa)[TI], const F(&fb)[TI]) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int j = 0; j < TI; ++j) acc[i][j] = TR ? mma(fa[i], fb[j], acc[i][j]) : mma(fb[j], fa[i], acc[i][j]);
+        if (sum_b) {
+            const F one = ones<F>();
+#pragma unroll
+            for (int j = 0; j < TI; ++j) dbs[j] = mma(fb[j], one, dbs[j]);
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            decltype(frag<T, AKC>(cur, 0, 0, 0)) fa[4], fb[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) fa[i] = frag<T, AKC>(cur, wr + 16 * i, s, lane);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) fb[j] = frag<T, BKC>(cur + kOpBytes, wc + 16 * j, s, lane);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = TR ? mma(fa[i], fb[j], acc[i][j]) : mma(fb[j], fa[i], acc[i][j]);
-            if (sum_b) {
-                const auto one = ones<decltype(frag<T, BKC>(cur, 0, 0, 0))>();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) dbs[j] = mma(fb[j], one, dbs[j]);
+    };
+    const int nk = int(kb1 - kb0);
+    auto k_of = [&](int kb) { return (kb0 + kb) * N::BK; };
+    if constexpr (NST == 4) {
+        // Stage kb of the ring is kb & 3.  At the top of block kb its stage and
+        // the next one are whole in LDS, the one after is in flight.  Fragments
+        // are read half a block (one step s) ahead of their MFMAs, across blocks too.
+        auto stage = [&](int kb) { return (kb & 3) * 2 * OPB; };
+        auto issue = [&](int kb) {       // past the end of k: zeros, which keeps the count of loads below
+            la.issue(k_of(kb), lds0 + stage(kb));
+            lb.issue(k_of(kb), lds0 + stage(kb) + OPB);
+        };
+        if (nk > 0) {
+            issue(0);
+            issue(1);
+            issue(2);
+            vm_wait<W / 16>();
+            __syncthreads();
+            F fa0[TI], fb0[TI], fa1[TI], fb1[TI];
+            read(smem + stage(0), 0, fa0, fb0);
+            for (int kb = 0; kb < nk; ++kb) {
+                issue(kb + 3);           // into the stage of block kb - 1, which every wave has read
+                read(smem + stage(kb), 1, fa1, fb1);
+                mul(fa0, fb0);
+                read(smem + stage(kb + 1), 0, fa0, fb0);
+                mul(fa1, fb1);
+                vm_wait<W / 16>();            // this wave's part of block kb + 2 has landed
+                __syncthreads();         // and every other wave's
             }
+            vm_wait<0>();                // no load may land after the epilogue reuses LDS or gives it away
         }
-        if (more) {
-            la.put(nxt);
-            lb.put(nxt + kOpBytes);
+    } else {
+        if (nk > 0) {
+            la.issue(k_of(0), lds0);
+            lb.issue(k_of(0), lds0 + OPB);
+            la.fetch(k_of(0));
+            lb.fetch(k_of(0));
+            la.put(smem);
+            lb.put(smem + OPB);
+        }
+        for (int kb = 0; kb < nk; ++kb) {
+            const int at = (kb & 1) * 2 * OPB, into = 2 * OPB - at;
+            vm_wait<0>();                // this wave's part of the stage has landed
+            __syncthreads();             // and every other wave's; the other stage has been read
+            const bool more = kb + 1 < nk;
+            if (more) {
+                la.issue(k_of(kb + 1), lds0 + into);
+                lb.issue(k_of(kb + 1), lds0 + into + OPB);
+                la.fetch(k_of(kb + 1));
+                lb.fetch(k_of(kb + 1));
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                F fa[TI], fb[TI];
+                read(smem + at, s, fa, fb);
+                mul(fa, fb);
+            }
+            if (more) {
+                la.put(smem + into);
+                lb.put(smem + into + OPB);
+            }
         }
     }
 
     const OutShape o = out_shape(a);
     const int g = lane >> 4, i16 = lane & 15;
-    const int64_t r0 = (TR ? t.tn : t.tm) * 128, c0 = (TR ? t.tm : t.tn) * 128;
+    const int64_t r0 = (TR ? t.tn : t.tm) * W, c0 = (TR ? t.tm : t.tn) * W;
     // f(row, column, values): runs of 8 of this wave's part of the output tile
     auto runs = [&](auto&& f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < TI / 2; ++p) {
                 float v[8];
                 if constexpr (TR) {
                     join_tiles(acc[2 * p][i], acc[2 * p + 1][i], v);
@@ -596,20 +645,20 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(LinArgs a) {
     };
     if (a.splits > 1) {
         runs([&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, r0 + r, c0 + c, v); });
-    } else if (KIND >= 0 && r0 + 128 <= o.rows && c0 + 128 <= o.cols && vector_epilogue(a)) {
+    } else if (KIND >= 0 && r0 + W <= o.rows && c0 + W <= o.cols && vector_epilogue(a)) {
         runs([&](int r, int c, float(&v)[8]) { epilogue8<16, KIND, true, N::dt>(a, r0 + r, c0 + c, 8, v); });
     } else {
         float* stage = reinterpret_cast<float*>(smem);
         __syncthreads();                 // every wave has read its last fragments
-        runs([&](int r, int c, float(&v)[8]) { stage_put(stage, 128, r, c, v); });
+        runs([&](int r, int c, float(&v)[8]) { stage_put(stage, W, r, c, v); });
         __syncthreads();
-        staged_epilogue<256>(a, o, stage, 128, 128, r0, c0);
+        staged_epilogue<256>(a, o, stage, W, W, r0, c0);
     }
     if (sum_b && i16 == 0) {   // every column of the product with ones is the same
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < TI; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) emit_db(a, t.split, t.tn * 128 + wc + 16 * j + 4 * g + e, dbs[j][e]);
+            for (int e = 0; e < 4; ++e) emit_db(a, t.split, t.tn * W + wc + 16 * j + 4 * g + e, dbs[j][e]);
     }
 }
 
@@ -647,7 +696,7 @@ struct HalfLoader {
     __device__ __forceinline__ int lrow(int q) const { return (wave * 2 + q) * (64 / CPR) + lane / CPR; }
     __device__ __forceinline__ int lchunk(int q) const {
         const int r = lrow(q), c = lane % CPR;
-        return KC ? c ^ (r & 7) : c ^ ks_swizzle<uint16_t>(r);
+        return KC ? c ^ (r & 7) : c ^ ks_swizzle<uint16_t, 128>(r);
     }
     __device__ __forceinline__ void init(const void* p, int64_t ld_, int64_t ext, int64_t e0, int64_t kend_, int wave_,
                                          int lane_) {
@@ -693,7 +742,7 @@ __device__ __forceinline__ uint32_t frag_base(int w0, int lane) {
     const int g = lane >> 4, i = lane & 15;
     if constexpr (KC) return uint32_t((w0 + i) * 128 + ((g ^ (i & 7)) << 4));
     const int k = 8 * g + (i >> 2), n = w0 + 4 * (i & 3);
-    return uint32_t(k * 256 + (((n >> 3) ^ ks_swizzle<uint16_t>(k)) << 4) + (n & 7) * 2);
+    return uint32_t(k * 256 + (((n >> 3) ^ ks_swizzle<uint16_t, 128>(k)) << 4) + (n & 7) * 2);
 }
 template <bool KC>
 __device__ __forceinline__ bf16x8_t frag_at(const char* smem, uint32_t base, int rc, int s, int region) {
@@ -939,9 +988,20 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int64_t out
 
 template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR>
 hipError_t launch_tile(const LinArgs& a, hipStream_t s) {
-    const int64_t nm = (a.M + 127) / 128, nn = (a.N + 127) / 128, all = nm * nn * a.splits;
-    hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, KIND, TR>), dim3(unsigned((all + 7) / 8 * 8)),
-                       dim3(256), 0, s, a);
+    const int64_t nm = (a.M + a.tile - 1) / a.tile, nn = (a.N + a.tile - 1) / a.tile, all = nm * nn * a.splits;
+    const dim3 grid(unsigned((all + 7) / 8 * 8)), block(256);
+    constexpr bool dma = ASRC == S_DMA && BSRC == S_DMA;
+    if (a.tile == 64) {
+        hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, KIND, TR, 64, dma ? 4 : 2>), grid, block, 0, s, a);
+    } else {
+        if constexpr (dma) {
+            if (a.deep) {
+                hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, KIND, TR, 128, 4>), grid, block, 0, s, a);
+                return hipGetLastError();
+            }
+        }
+        hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, KIND, TR, 128, 2>), grid, block, 0, s, a);
+    }
     return hipGetLastError();
 }
 template <bool AKC, bool BKC, int KIND, bool TR>
@@ -985,49 +1045,67 @@ hipError_t launch_typed(const LinArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Tile edge and split of a product: the cheapest by a model of its time in us.
-// A wave of 128-wide tiles (two workgroups a CU) takes about 4 + 1.05 per k
-// block of 64, and less while each CU holds one workgroup; a wave of 256-wide
-// ones (one a CU) about 10 + 1.3 (1.25 where both operands are row-contiguous)
-// for twice the output.  Measured, bf16: 8192 x 1024 -> 4096 88 us on 128-wide
-// tiles, 74 on 256-wide ones; 4096 x 14336 -> 4096 440 and 374 (429 and 315
-// row-contiguous); 2048 x 2048 -> 1408, whose 48 wide tiles leave most CUs idle,
-// 28 and 52.  A split adds the second kernel's launch and its sums' traffic.
-// An 8-bit operand is decoded by the 128-wide kernel itself, which more than
-// doubles its time per k block, or by a pass of its own into the workspace
-// (8192 tokens, 1024 x 4096, 128-wide: 215 us fused, 95 + 7 in two passes).
+// Tile edge and split of a product: the cheapest by a model of its time in us,
+// fitted to graph replays on one MI355X.  A tile takes a fixed time (launch,
+// first loads, epilogue) and a time per k block of 128 bytes a row, which grows
+// with the workgroups that share a CU:
+//
+//   edge  fixed  per k block: bf16 (weight gradient)  float32
+//     64   3.5     0.25 (0.40)                          0.45
+//    128   5.5     0.50 (0.75), 0.58 shared             1.75
+//    256   11      1.42, 1.30 both row-contiguous (1.50)
+//
+// No product is faster than its operands' bytes at 5 TB/s.  A split adds the
+// joining kernel (4 us and its sums' bytes).  Both sides, measured: 1024 x 1024
+// -> 1024 8.5 us on 64-wide tiles, 13 on 128-wide ones, 14 split in two; 2048 x
+// 2048 -> 1408 26, 23 and 52 us on 64, 128 and 256; 4096 x 4096 -> 4096 150 us on
+// 128, 106 on 256.
+// An 8-bit operand is decoded by the product itself, which more than doubles its
+// time per k block, or by a pass of its own into the workspace (8192 tokens,
+// 1024 x 4096: 215 us fused, 95 + 7 in two passes, on 128-wide tiles).
+struct TileCost {
+    int edge;
+    double fixed, block, block_dw, block_f32;
+};
+constexpr TileCost kTileCosts[] = {{64, 3.5, 0.25, 0.40, 0.45}, {128, 5.5, 0.50, 0.75, 1.75}, {256, 11, 1.42, 1.50, 0}};
+
 LinPlan plan_linear(const LinArgs& a) {
     LinPlan best;
     double best_us = 1e30;
     const OutShape o = out_shape(a);
+    const int64_t bk = a.dt == 0 ? 64 : 32, nkb = (a.K + bk - 1) / bk;
+    const double es = a.dt == 0 ? 2 : 4;
+    const double bytes_us = (double(a.M) * double(a.K) + double(a.K) * double(a.N)) * es / 5e6;
     for (int decode = 0; decode <= (a.a_exps && a.dt == 0 ? 1 : 0); ++decode) {
-    const bool a_dma = decode ? true : a.a_dma != 0, fused8 = a.a_exps && !decode;
-    const bool wide_ok = a.dt == 0 && a_dma && a.b_dma;
-    const int64_t nkb = (a.K + (a.dt == 0 ? 64 : 32) - 1) / (a.dt == 0 ? 64 : 32);
-    for (int tile : {128, 256}) {
-        if (tile == 256 && !wide_ok) continue;
-        const int64_t tiles = ((a.M + tile - 1) / tile) * ((a.N + tile - 1) / tile);
-        const int64_t slots = tile == 256 ? 256 : 512;
-        // a split keeps at least 4 k blocks and at most fills the slots once
-        int64_t most = std::min<int64_t>(std::min<int64_t>(nkb / 4, slots / tiles), 64);
-        for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
-            const int64_t per = (nkb + s - 1) / s;
-            if (s > 1 && (nkb + per - 1) / per != s) continue;   // it would leave a split empty
-            const int64_t wgs = tiles * s;
-            double us;
-            if (tile == 256) us = double((wgs + 255) / 256) * (10 + (a.a_kc && a.b_kc ? 1.25 : 1.35) * double(per));
-            else us = double((wgs + 511) / 512) * (4 + (wgs <= 256 ? 0.75 : 1.05) * (a.dt == 0 ? 1.0 : 2.5) *
-                                                               (fused8 ? 2.3 : 1.0) * double(per));
-            if (decode) us += 2 + double(a.K) * double(a.M) * 3 / 4.5e6;
-            if (s > 1) us += 4 + double(s) * double(o.rows) * double(o.ldp) * 8 / 4.5e6;
-            if (us < best_us) {
-                best_us = us;
-                best.tile = tile;
-                best.splits = int(s);
-                best.decode_ld = decode ? (a.M + 7) / 8 * 8 : 0;
+        const bool a_dma = decode || a.a_dma, fused8 = a.a_exps && !decode, dma = a_dma && a.b_dma;
+        for (const TileCost& tc : kTileCosts) {
+            if (tc.edge == 256 && (a.dt != 0 || !dma)) continue;
+            const int64_t tiles = ((a.M + tc.edge - 1) / tc.edge) * ((a.N + tc.edge - 1) / tc.edge);
+            double block = a.dt != 0 ? tc.block_f32 : a.kind == LIN_DW ? tc.block_dw : tc.block;
+            if (tc.edge == 256 && a.a_kc && a.b_kc) block = 1.30;
+            if (!dma) block *= fused8 && a.b_dma ? 2.3 : 3.0;
+            // a split keeps at least 2 k blocks and at most fills two workgroups a CU
+            const int64_t most = std::min<int64_t>(std::min<int64_t>(nkb / 2, 512 / tiles), 64);
+            for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
+                const int64_t per = (nkb + s - 1) / s;
+                if (s > 1 && (nkb + per - 1) / per != s) continue;   // it would leave a split empty
+                const double w = double(tiles * s) / 256;            // workgroups a CU
+                double us;
+                if (tc.edge == 256) us = 3 + std::ceil(w) * (tc.fixed + block * double(per));
+                else if (tc.edge == 64 || w <= 1) us = tc.fixed + block * std::max(w, 1.0) * double(per);
+                else us = tc.fixed + 1.16 * block * 2 * std::ceil(w / 2) * double(per);
+                us = std::max(us, bytes_us);
+                if (s > 1) us += 4 + double(s) * double(o.rows) * double(o.ldp) * 8 / 5e6;
+                if (decode) us += 2 + double(a.K) * double(a.M) * 3 / 5e6;
+                if (us < best_us) {
+                    best_us = us;
+                    best.tile = tc.edge;
+                    best.splits = int(s);
+                    best.deep = tiles * s <= 256;
+                    best.decode_ld = decode ? (a.M + 7) / 8 * 8 : 0;
+                }
             }
         }
-    }
     }
     best.decode_bytes = size_t(best.decode_ld) * size_t(a.K) * 2;
     if (best.splits > 1) {
