@@ -217,14 +217,17 @@ muon_status run_linear(HandleBase* h, LinArgs& a, hipStream_t stream) {
     a.deep = p.deep;
     void* ws = nullptr;
     auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-    const size_t pb = up(p.partial_bytes), bb = up(p.db_bytes);
-    const muon_status st = workspace(h, pb + bb + p.decode_bytes, stream, &ws);
+    const size_t at[4] = {0, up(p.partial_bytes), up(p.partial_bytes) + up(p.db_bytes),
+                          up(p.partial_bytes) + up(p.db_bytes) + up(p.a_bytes)};
+    const muon_status st = workspace(h, at[3] + p.b_bytes, stream, &ws);
     if (st != MUON_OK) return st;
     char* base = static_cast<char*>(ws);
-    a.partial = reinterpret_cast<float*>(base);
-    a.db_partial = p.db_bytes ? reinterpret_cast<float*>(base + pb) : nullptr;
-    a.decoded = p.decode_ld ? base + pb + bb : nullptr;
-    a.decode_ld = p.decode_ld;
+    if (p.partial_bytes) a.partial = reinterpret_cast<float*>(base);
+    if (p.db_bytes) a.db_partial = reinterpret_cast<float*>(base + at[1]);
+    if (p.a_bytes) a.a_ws = base + at[2];
+    if (p.b_bytes) a.b_ws = base + at[3];
+    a.a_ld = p.a_ld;
+    a.b_ld = p.b_ld;
     const hipError_t e = launch_linear(a, stream);
     if (e != hipSuccess) return hip_fail(h, e, "linear launch");
     return MUON_OK;

@@ -127,20 +127,23 @@ struct LinArgs {
     // (float32, [splits][rows][cols] of the output's orientation, then
     // [splits][N] of the column sums) and a second kernel joins them
     int32_t splits;
-    int32_t tile;              // tile edge: 128 or 256
-    int32_t deep;              // 128-wide tiles: four LDS stages, one workgroup a CU
+    int32_t tile;              // tile edge: 64, 128 or 256
+    int32_t deep;              // no more workgroups than CUs: more LDS stages
     float* partial;
     float* db_partial;
-    void* decoded;             // A decoded from 8 bits, K rows of decode_ld bf16; 0: decoded by the product
-    int64_t decode_ld;
+    // operands re-laid in the workspace before the product, as stored but with
+    // aligned rows of a_ld / b_ld elements; 0: taken as they are
+    void* a_ws;
+    void* b_ws;
+    int64_t a_ld, b_ld;
 };
 
 struct LinPlan {
     int tile = 128;
     int splits = 1;
     bool deep = false;
-    int64_t decode_ld = 0;
-    size_t partial_bytes = 0, db_bytes = 0, decode_bytes = 0;
+    int64_t a_ld = 0, b_ld = 0;
+    size_t partial_bytes = 0, db_bytes = 0, a_bytes = 0, b_bytes = 0;
 };
 LinPlan plan_linear(const LinArgs& a);
 hipError_t launch_linear(const LinArgs& a, hipStream_t s);

@@ -504,8 +504,9 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs& a, int edge) {
 // and two stages (64 KB) two workgroups share a CU and one's epilogue and waits
 // overlap the other's MFMAs.  Where there are no more workgroups than CUs, four
 // stages (128 KB) let the fragments be read half a block ahead (below): 2048 x
-// 2048 -> 1408 28 -> 23 us.  W = 64 with four stages (64 KB) serves outputs of
-// few tiles.
+// 2048 -> 1408 28 -> 23 us.  W = 64 serves outputs of few tiles, with four stages
+// (64 KB), or eight where a CU has only one workgroup: a few rows' product is as
+// fast as the weight arrives, and that takes 7 blocks in flight on each CU.
 // TR: the accumulators hold runs along M (the output is stored transposed).
 // ---------------------------------------------------------------------------
 template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR, int W, int NST>
@@ -563,30 +564,32 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
     };
     const int nk = int(kb1 - kb0);
     auto k_of = [&](int kb) { return (kb0 + kb) * N::BK; };
-    if constexpr (NST == 4) {
-        // Stage kb of the ring is kb & 3.  At the top of block kb its stage and
-        // the next one are whole in LDS, the one after is in flight.  Fragments
-        // are read half a block (one step s) ahead of their MFMAs, across blocks too.
-        auto stage = [&](int kb) { return (kb & 3) * 2 * OPB; };
+    if constexpr (NST >= 4) {
+        // Stage kb of the ring is kb mod NST.  At the top of block kb its stage and
+        // the next one are whole in LDS, the NST - 3 after them are in flight.
+        // Fragments are read half a block (one step s) ahead of their MFMAs,
+        // across blocks too.
+        static_assert((NST & (NST - 1)) == 0, "ring");
+        constexpr int kFlight = (NST - 3) * (W / 16);   // a wave's loads of those blocks
+        auto stage = [&](int kb) { return (kb & (NST - 1)) * 2 * OPB; };
         auto issue = [&](int kb) {       // past the end of k: zeros, which keeps the count of loads below
             la.issue(k_of(kb), lds0 + stage(kb));
             lb.issue(k_of(kb), lds0 + stage(kb) + OPB);
         };
         if (nk > 0) {
-            issue(0);
-            issue(1);
-            issue(2);
-            vm_wait<W / 16>();
+#pragma unroll
+            for (int p = 0; p < NST - 1; ++p) issue(p);
+            vm_wait<kFlight>();
             __syncthreads();
             F fa0[TI], fb0[TI], fa1[TI], fb1[TI];
             read(smem + stage(0), 0, fa0, fb0);
             for (int kb = 0; kb < nk; ++kb) {
-                issue(kb + 3);           // into the stage of block kb - 1, which every wave has read
+                issue(kb + NST - 1);     // into the stage of block kb - 1, which every wave has read
                 read(smem + stage(kb), 1, fa1, fb1);
                 mul(fa0, fb0);
                 read(smem + stage(kb + 1), 0, fa0, fb0);
                 mul(fa1, fb1);
-                vm_wait<W / 16>();            // this wave's part of block kb + 2 has landed
+                vm_wait<kFlight>();      // this wave's part of block kb + 2 has landed
                 __syncthreads();         // and every other wave's
             }
             vm_wait<0>();                // no load may land after the epilogue reuses LDS or gives it away
@@ -986,12 +989,50 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int64_t out
     epilogue8<1, -1, false, -1>(a, r, c, n > 0 ? int(n) : 0, v);
 }
 
+// An operand with rows that are not whole aligned 16-byte chunks, copied into
+// the workspace with such rows (their ends zero): 16 bytes a lane.
+template <class T>
+__global__ __launch_bounds__(256) void linear_pack_kernel(const T* src, int64_t ld, T* dst, int64_t ldd, int64_t rows,
+                                                          int64_t cols) {
+    constexpr int E = Num<T>::EPC;
+    const int64_t cpr = ldd / E, i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t r = i / cpr, c = (i - r * cpr) * E;
+    if (r >= rows) return;
+    const GMEM T* p = gm(src) + r * ld + c;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (c + e < cols) {
+            if constexpr (Num<T>::dt == 0) w[e / 2] |= uint32_t(p[e]) << (16 * (e & 1));
+            else w[e] = __float_as_uint(p[e]);
+        }
+    *reinterpret_cast<GMEM u32x4_t*>(gm(dst) + r * ldd + c) = u32x4_t{w[0], w[1], w[2], w[3]};
+}
+hipError_t launch_pack(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int64_t cols, int dt,
+                       hipStream_t s) {
+    const int64_t n = rows * (ldd / (dt == 0 ? 8 : 4));
+    const dim3 grid(unsigned((n + 255) / 256)), block(256);
+    if (dt == 0)
+        hipLaunchKernelGGL((linear_pack_kernel<uint16_t>), grid, block, 0, s, static_cast<const uint16_t*>(src), ld,
+                           static_cast<uint16_t*>(dst), ldd, rows, cols);
+    else
+        hipLaunchKernelGGL((linear_pack_kernel<float>), grid, block, 0, s, static_cast<const float*>(src), ld,
+                           static_cast<float*>(dst), ldd, rows, cols);
+    return hipGetLastError();
+}
+
 template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR>
 hipError_t launch_tile(const LinArgs& a, hipStream_t s) {
     const int64_t nm = (a.M + a.tile - 1) / a.tile, nn = (a.N + a.tile - 1) / a.tile, all = nm * nn * a.splits;
     const dim3 grid(unsigned((all + 7) / 8 * 8)), block(256);
     constexpr bool dma = ASRC == S_DMA && BSRC == S_DMA;
     if (a.tile == 64) {
+        if constexpr (dma) {
+            if (a.deep) {
+                hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, KIND, TR, 64, 8>), grid, block, 0, s, a);
+                return hipGetLastError();
+            }
+        }
         hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, ASRC, BSRC, KIND, TR, 64, dma ? 4 : 2>), grid, block, 0, s, a);
     } else {
         if constexpr (dma) {
@@ -1060,9 +1101,12 @@ hipError_t launch_typed(const LinArgs& a, hipStream_t s) {
 // -> 1024 8.5 us on 64-wide tiles, 13 on 128-wide ones, 14 split in two; 2048 x
 // 2048 -> 1408 26, 23 and 52 us on 64, 128 and 256; 4096 x 4096 -> 4096 150 us on
 // 128, 106 on 256.
-// An 8-bit operand is decoded by the product itself, which more than doubles its
-// time per k block, or by a pass of its own into the workspace (8192 tokens,
-// 1024 x 4096: 215 us fused, 95 + 7 in two passes, on 128-wide tiles).
+// An 8-bit operand is decoded by the product itself, which doubles its time per
+// k block, or by a pass of its own into the workspace (1024 x 1000, 500 tokens:
+// 9.8 us by itself, 13 in two passes; 4000 tokens: 34 and 32).  Operands without
+// whole aligned chunks are read element by element by the product, about nine
+// times slower per k block, or copied first to rows that have them (4000 x 3001
+// -> 2047: 480 and 89 us; 1 x 2001 -> 999: 14 and 17).
 struct TileCost {
     int edge;
     double fixed, block, block_dw, block_f32;
@@ -1076,14 +1120,23 @@ LinPlan plan_linear(const LinArgs& a) {
     const int64_t bk = a.dt == 0 ? 64 : 32, nkb = (a.K + bk - 1) / bk;
     const double es = a.dt == 0 ? 2 : 4;
     const double bytes_us = (double(a.M) * double(a.K) + double(a.K) * double(a.N)) * es / 5e6;
-    for (int decode = 0; decode <= (a.a_exps && a.dt == 0 ? 1 : 0); ++decode) {
-        const bool a_dma = decode || a.a_dma, fused8 = a.a_exps && !decode, dma = a_dma && a.b_dma;
+    // rows and columns of the operands as stored, and their re-laid leading dimensions
+    const int64_t ar = a.a_kc ? a.M : a.K, ac = a.a_kc ? a.K : a.M, br = a.b_kc ? a.N : a.K, bc = a.b_kc ? a.K : a.N;
+    const int64_t chunk = a.dt == 0 ? 8 : 4, lda = (ac + chunk - 1) / chunk * chunk, ldb = (bc + chunk - 1) / chunk * chunk;
+    // operands taken as they are (0), or those that need it re-laid first (1): an
+    // 8-bit one decoded, a ragged or misaligned one packed
+    const bool plain = a.a_dma && a.b_dma;
+    for (int relay = 0; relay <= (plain ? 0 : 1); ++relay) {
+        const bool fused8 = a.a_exps && !relay, dma = relay || plain;
+        double relay_us = 0;
+        if (relay && !a.a_dma) relay_us += 4 + double(ar) * double(ac) * es * (a.a_exps ? 1.5 : 2) / 4.5e6;
+        if (relay && !a.b_dma) relay_us += 4 + double(br) * double(bc) * es * 2 / 4.5e6;
         for (const TileCost& tc : kTileCosts) {
             if (tc.edge == 256 && (a.dt != 0 || !dma)) continue;
             const int64_t tiles = ((a.M + tc.edge - 1) / tc.edge) * ((a.N + tc.edge - 1) / tc.edge);
             double block = a.dt != 0 ? tc.block_f32 : a.kind == LIN_DW ? tc.block_dw : tc.block;
             if (tc.edge == 256 && a.a_kc && a.b_kc) block = 1.30;
-            if (!dma) block *= fused8 && a.b_dma ? 2.3 : 3.0;
+            if (!dma) block *= fused8 && a.b_dma ? 2.0 : 9.0;
             // a split keeps at least 2 k blocks and at most fills two workgroups a CU
             const int64_t most = std::min<int64_t>(std::min<int64_t>(nkb / 2, 512 / tiles), 64);
             for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
@@ -1096,18 +1149,20 @@ LinPlan plan_linear(const LinArgs& a) {
                 else us = tc.fixed + 1.16 * block * 2 * std::ceil(w / 2) * double(per);
                 us = std::max(us, bytes_us);
                 if (s > 1) us += 4 + double(s) * double(o.rows) * double(o.ldp) * 8 / 5e6;
-                if (decode) us += 2 + double(a.K) * double(a.M) * 3 / 5e6;
+                us += relay_us;
                 if (us < best_us) {
                     best_us = us;
                     best.tile = tc.edge;
                     best.splits = int(s);
                     best.deep = tiles * s <= 256;
-                    best.decode_ld = decode ? (a.M + 7) / 8 * 8 : 0;
+                    best.a_ld = relay && !a.a_dma ? lda : 0;
+                    best.b_ld = relay && !a.b_dma ? ldb : 0;
                 }
             }
         }
     }
-    best.decode_bytes = size_t(best.decode_ld) * size_t(a.K) * 2;
+    best.a_bytes = size_t(best.a_ld) * size_t(ar) * size_t(es);
+    best.b_bytes = size_t(best.b_ld) * size_t(br) * size_t(es);
     if (best.splits > 1) {
         best.partial_bytes = size_t(best.splits) * size_t(o.rows) * size_t(o.ldp) * 4;
         best.db_bytes = a.db ? size_t(best.splits) * size_t(a.N) * 4 : 0;
@@ -1118,23 +1173,37 @@ LinPlan plan_linear(const LinArgs& a) {
 hipError_t launch_linear(const LinArgs& args, hipStream_t s) {
     LinArgs a = args;
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
-    if (a.decode_ld) {   // the 8-bit operand as bf16 rows in the workspace
-        Act8Args q;
-        q.x = nullptr;
-        q.y = a.decoded;
-        q.q = Act8View{static_cast<int8_t*>(const_cast<void*>(a.a)), const_cast<uint8_t*>(a.a_exps), a.lda, a.lda_exps,
-                       a.a8_vec};
-        q.rows = a.K;
-        q.ld = a.decode_ld;
-        q.cols = int32_t(a.M);
-        q.dt = 0;
-        q.vec = a.a8_vec;
-        const hipError_t d = launch_act8_decode(q, s);
+    if (a.a_ld) {        // re-lay A in the workspace
+        const int64_t rows = a.a_kc ? a.M : a.K, cols = a.a_kc ? a.K : a.M;
+        hipError_t d;
+        if (a.a_exps) {
+            Act8Args q;
+            q.x = nullptr;
+            q.y = a.a_ws;
+            q.q = Act8View{static_cast<int8_t*>(const_cast<void*>(a.a)), const_cast<uint8_t*>(a.a_exps), a.lda,
+                           a.lda_exps, a.a8_vec};
+            q.rows = rows;
+            q.ld = a.a_ld;
+            q.cols = int32_t(cols);
+            q.dt = a.dt;
+            q.vec = a.a8_vec;
+            d = launch_act8_decode(q, s);
+        } else {
+            d = launch_pack(a.a, a.lda, a.a_ws, a.a_ld, rows, cols, a.dt, s);
+        }
         if (d != hipSuccess) return d;
-        a.a = a.decoded;
-        a.lda = a.decode_ld;
+        a.a = a.a_ws;
+        a.lda = a.a_ld;
         a.a_exps = nullptr;
         a.a_dma = 1;
+    }
+    if (a.b_ld) {
+        const hipError_t d =
+            launch_pack(a.b, a.ldb, a.b_ws, a.b_ld, a.b_kc ? a.N : a.K, a.b_kc ? a.K : a.N, a.dt, s);
+        if (d != hipSuccess) return d;
+        a.b = a.b_ws;
+        a.ldb = a.b_ld;
+        a.b_dma = 1;
     }
     hipError_t e = a.tile == 256 ? launch_256(a, s)
                                  : (a.dt == 0 ? launch_typed<uint16_t>(a, s) : launch_typed<float>(a, s));

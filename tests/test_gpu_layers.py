@@ -273,7 +273,7 @@ def lin_tol(k, mag, act_mag, y, st):
 
 LIN_SHAPES = [(1, 1, 1), (1, 64, 8), (1, 1024, 384), (2, 40, 72), (16, 256, 128), (17, 100, 50), (64, 512, 512),
               (127, 129, 131), (128, 128, 128), (130, 200, 264), (255, 72, 520), (300, 768, 768), (513, 1408, 264),
-              (40, 4096, 136), (1, 333, 999)]
+              (40, 4096, 136), (1, 333, 999), (900, 1001, 1031), (16, 2051, 776)]
 
 
 def act_slope(z, kind):
@@ -357,7 +357,7 @@ def test_linear_grad_input(nsm, h, rows, k, n, layout, st):
 
 
 DW_SHAPES = [(1, 1, 1), (1, 8, 16), (5, 40, 72), (33, 131, 67), (64, 128, 128), (100, 200, 264), (257, 256, 136),
-             (1000, 96, 520), (4100, 72, 40), (513, 1408, 264)]
+             (1000, 96, 520), (4100, 72, 40), (513, 1408, 264), (1300, 1001, 771)]
 
 
 @pytest.mark.parametrize("st", ["bf16", "fp32"])
