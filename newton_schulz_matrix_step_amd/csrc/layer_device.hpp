@@ -128,14 +128,15 @@ __device__ __forceinline__ float act_value(float z, int act) {
 }
 // Value and derivative.  With e = exp(-u), s = 1 / (1 + e) and 1 - s = e s (no
 // cancellation).  Beyond |z| = 9 the derivative is 0 or 1 to float32 (e^66 or
-// e^-66 away), and nothing below can overflow.
+// e^-66 away) and z is held there, so that nothing can overflow; adding 0 z
+// lets a NaN through the clamp.
 __device__ __forceinline__ void act_both(float z, int act, float& v, float& d) {
     if (act == ACT_GELU) {
-        const float c = z < -9.f ? -9.f : (z > 9.f ? 9.f : z);   // a NaN stays one
-        const float e = gelu_exp(c);
+        const float c = __builtin_amdgcn_fmed3f(z, -9.f, 9.f), c2 = c * c;
+        const float e = __builtin_amdgcn_exp2f(c * fmaf(kGeluE3, c2, kGeluE1));
         const float s = __builtin_amdgcn_rcpf(1.f + e);
-        v = (z > 0.f ? z : c) * s;
-        d = fmaf(c * s * (e * s), kGeluU * fmaf(3.f * kGeluC * c, c, 1.f), s);
+        v = fmaf(z, 0.f, __builtin_fmaxf(z, c) * s);
+        d = fmaf(z, 0.f, fmaf((c * s) * (e * s), fmaf(3.f * kGeluC * kGeluU, c2, kGeluU), s));
     } else if (act == ACT_RELU_SQ) {
         v = z <= 0.f ? 0.f : z * z;
         d = z <= 0.f ? 0.f : 2.f * z;

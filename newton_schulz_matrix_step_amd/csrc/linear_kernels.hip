@@ -150,24 +150,23 @@ struct Loader {
         }
     }
 
-    // S_DMA: enqueue the stage at k0 into LDS at address st
-    __device__ __forceinline__ void issue(int64_t k0, uint32_t st) {
+    // S_DMA: enqueue block q of the stage at k0 into LDS at address st, or all of it
+    __device__ __forceinline__ void issue(int64_t k0, uint32_t st, int q) {
         if constexpr (SRC == S_DMA) {
+            const uint32_t at = st + (wave * NQ + q) * 1024;
             if constexpr (KC) {
-                const i32x4_t buf = buffer_at(base + k0 * ES, kMaxRecords);
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    const bool in = k0 + lchunk(q) * N::EPC < kend;   // a whole chunk is in or out
-                    buffer_to_lds(buf, in ? voff[q] : kFar, st + (wave * NQ + q) * 1024);
-                }
+                const bool in = k0 + lchunk(q) * N::EPC < kend;   // a whole chunk is in or out
+                buffer_to_lds(buffer_at(base + k0 * ES, kMaxRecords), in ? voff[q] : kFar, at);
             } else {
                 int64_t n = (kend - k0) * ld * ES;   // rows past kend lie past the buffer
                 n = n < 0 ? 0 : (n > int64_t(kMaxRecords) ? int64_t(kMaxRecords) : n);
-                const i32x4_t buf = buffer_at(base + k0 * ld * ES, uint32_t(n));
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) buffer_to_lds(buf, voff[q], st + (wave * NQ + q) * 1024);
+                buffer_to_lds(buffer_at(base + k0 * ld * ES, uint32_t(n)), voff[q], at);
             }
         }
+    }
+    __device__ __forceinline__ void issue(int64_t k0, uint32_t st) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) issue(k0, st, q);
     }
 
     // S_ANY, S_ACT8: load the stage at k0 into registers
@@ -319,64 +318,173 @@ __device__ __forceinline__ void join_tiles(f32x4_t a, f32x4_t b, float (&v)[8]) 
     }
 }
 
-// 8 consecutive elements (r, c ..) of the output, nv of them inside (0: none).
-// SH: lane distance between the four lanes that share a group of 32 columns.
-// KIND: the product, or -1 to take it from the arguments.  FAST: all 8 elements
-// lie inside and every buffer of the epilogue allows vectors (see fast_epilogue).
-// DT: the tensors' type (a Num's dt), or -1 to take that from the arguments.
-template <int SH, int KIND, bool FAST, int DT>
-__device__ __forceinline__ void epilogue8(const LinArgs& a, int64_t r, int64_t c, int nv, float (&v)[8]) {
-    const int kind = KIND >= 0 ? KIND : a.kind;
-    const int dt = DT >= 0 ? DT : a.dt, out_dt = kind == LIN_DW ? a.out_dt : dt;
-    if (FAST) nv = 8;
-    if (kind == LIN_FWD) {
+// Where a run of 8 consecutive output elements lies: row r + rl, columns c + cl ..
+// of the output, r and c the same for all lanes.  An address is then a scalar
+// base plus a 32-bit lane offset that stays the same from run to run.
+struct RunAt {
+    int64_t r, c;
+    int rl, cl;
+};
+// Byte address of that run in a matrix of `es`-byte elements.
+template <class B>
+__device__ __forceinline__ GMEM B* run_ptr(B* p, int64_t ld, const RunAt& t, int es) {
+    return gm(reinterpret_cast<B*>(const_cast<char*>(reinterpret_cast<const char*>(p)) + (t.r * ld + t.c) * es)) +
+           (uint32_t(t.rl) * uint32_t(ld) + uint32_t(t.cl)) * uint32_t(es);
+}
+template <int DT>
+__device__ __forceinline__ void run_load(const void* p, int64_t ld, const RunAt& t, int dt_arg, float (&v)[8]) {
+    const int dt = DT >= 0 ? DT : dt_arg;
+    const GMEM char* q = run_ptr(static_cast<const char*>(p), ld, t, dt == 0 ? 2 : 4);
+    if (dt == 0) {
+        unpack_bf16x8(*reinterpret_cast<const GMEM u32x4_t*>(q), v);
+    } else {
+        const f32x4_t a = *reinterpret_cast<const GMEM f32x4_t*>(q), b = *reinterpret_cast<const GMEM f32x4_t*>(q + 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = a[k];
+            v[4 + k] = b[k];
+        }
+    }
+}
+template <int DT>
+__device__ __forceinline__ void run_store(void* p, int64_t ld, const RunAt& t, int dt_arg, const float (&v)[8]) {
+    const int dt = DT >= 0 ? DT : dt_arg;
+    GMEM char* q = run_ptr(static_cast<char*>(p), ld, t, dt == 0 ? 2 : 4);
+    if (dt == 0) {
+        *reinterpret_cast<GMEM u32x4_t*>(q) =
+            u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    } else {
+        *reinterpret_cast<GMEM f32x4_t*>(q) = f32x4_t{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<GMEM f32x4_t*>(q + 16) = f32x4_t{v[4], v[5], v[6], v[7]};
+    }
+}
+template <int SH>
+__device__ __forceinline__ float group_max(const float (&v)[8], int nv) {
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max_mag(m, k < nv ? v[k] : 0.f);
+    m = max_mag(m, __shfl_xor(m, SH, 64));
+    return max_mag(m, __shfl_xor(m, 2 * SH, 64));
+}
+__device__ __forceinline__ u32x2_t act8_pack(const float (&v)[8], uint32_t e, int nv) {
+    u32x2_t w = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k >> 2] |= (k < nv ? act8_code(v[k], e) : 0u) << (8 * (k & 3));
+    return w;
+}
+__device__ __forceinline__ void act_all(float (&v)[8], int act) {
+    if (act == ACT_GELU) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], ACT_GELU);
+    } else if (act == ACT_RELU_SQ) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], ACT_RELU_SQ);
+    }
+}
+// v *= act'(z), h = act(z)
+__device__ __forceinline__ void act_grad_all(float (&v)[8], const float (&z)[8], float (&h)[8], int act) {
+    float d[8];
+    if (act == ACT_GELU) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) act_both(z[k], ACT_GELU, h[k], d[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) act_both(z[k], act, h[k], d[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= d[k];
+}
+
+// The run's 8 elements, all inside, every buffer of the epilogue allowing
+// vectors and 32-bit offsets (fast_epilogue).  The four lanes of a group of 32
+// columns lie 16 apart.
+template <int KIND, int DT>
+__device__ __forceinline__ void epilogue_run(const LinArgs& a, const RunAt& t, float (&v)[8]) {
+    if (KIND == LIN_FWD) {
         if (a.bias) {
             float b[8];
-            load8(a.bias, c, a.bias_dt, FAST, nv, b);
+            const RunAt tb{0, t.c, 0, t.cl};
+            if (a.bias_dt == 0) run_load<0>(a.bias, 0, tb, 0, b);
+            else run_load<1>(a.bias, 0, tb, 1, b);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += b[k];
         }
-        if (a.z && nv > 0) store8(a.z, r * a.ld_z + c, dt, FAST || a.z_vec, nv, v);
+        if (a.z) run_store<DT>(a.z, a.ld_z, t, DT, v);
         if (a.z8.codes) {
-            float m = 0.f;
+            const uint32_t e = act8_exp(group_max<16>(v, 8));
+            *reinterpret_cast<GMEM u32x2_t*>(run_ptr(a.z8.codes, a.z8.ld, t, 1)) = act8_pack(v, e, 8);
+            if ((t.cl & (kAct8Group - 1)) == 0)
+                *run_ptr(a.z8.exps, a.z8.lde, RunAt{t.r, t.c / kAct8Group, t.rl, t.cl / kAct8Group}, 1) = uint8_t(e);
+        }
+        act_all(v, a.act);
+    } else if (KIND == LIN_DX) {
+        if (a.z || a.z8.codes) {
+            float z[8], h[8];
+            if (a.z) {
+                run_load<DT>(a.z, a.ld_z, t, DT, z);
+            } else {
+                const float step =
+                    act8_step(*run_ptr(a.z8.exps, a.z8.lde, RunAt{t.r, t.c / kAct8Group, t.rl, t.cl / kAct8Group}, 1));
+                const u32x2_t w = *reinterpret_cast<const GMEM u32x2_t*>(run_ptr(a.z8.codes, a.z8.ld, t, 1));
+                act8_dec4(w[0], step, z);
+                act8_dec4(w[1], step, z + 4);
+            }
+            act_grad_all(v, z, h, a.act);
+            if (a.act_out) run_store<DT>(a.act_out, a.ld_act, t, DT, h);
+        }
+    } else if (a.accumulate) {
+        float o[8];
+        run_load<-1>(a.out, a.ld_out, t, a.out_dt, o);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) m = max_mag(m, k < nv ? v[k] : 0.f);
-            m = max_mag(m, __shfl_xor(m, SH, 64));
-            m = max_mag(m, __shfl_xor(m, 2 * SH, 64));
+        for (int k = 0; k < 8; ++k) v[k] += o[k];
+    }
+    if (KIND != LIN_DW && a.add) {
+        float b[8];
+        run_load<DT>(a.add, a.ld_add, t, DT, b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += b[k];
+    }
+    run_store<KIND == LIN_DW ? -1 : DT>(a.out, a.ld_out, t, a.out_dt, v);
+}
+
+// Any run: 8 elements from (r, c) on, nv of them inside (0: none), any
+// alignment.  The four lanes of a group of 32 columns are neighbours.
+__device__ __forceinline__ void epilogue_any(const LinArgs& a, int64_t r, int64_t c, int nv, float (&v)[8]) {
+    if (a.kind == LIN_FWD) {
+        if (a.bias) {
+            float b[8];
+            load8(a.bias, c, a.bias_dt, a.bias_vec, nv, b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] += b[k];
+        }
+        if (a.z && nv > 0) store8(a.z, r * a.ld_z + c, a.dt, a.z_vec, nv, v);
+        if (a.z8.codes) {
+            const uint32_t e = act8_exp(group_max<1>(v, nv));
             if (nv > 0) {
-                const uint32_t e = act8_exp(m);
+                const u32x2_t w = act8_pack(v, e, nv);
                 GMEM int8_t* p = gm(a.z8.codes) + r * a.z8.ld + c;
-                if (FAST || (a.z8.vec && nv >= 8)) {
-                    u32x2_t w = {0u, 0u};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k >> 2] |= act8_code(v[k], e) << (8 * (k & 3));
+                if (a.z8.vec && nv >= 8) {
                     *reinterpret_cast<GMEM u32x2_t*>(p) = w;
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (k < nv) p[k] = int8_t(act8_code(v[k], e));
+                        if (k < nv) p[k] = int8_t(w[k >> 2] >> (8 * (k & 3)));
                 }
                 if ((c & (kAct8Group - 1)) == 0) gm(a.z8.exps)[r * a.z8.lde + c / kAct8Group] = uint8_t(e);
             }
         }
         if (nv <= 0) return;
-        if (a.act == ACT_GELU) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], ACT_GELU);
-        } else if (a.act == ACT_RELU_SQ) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = act_value(v[k], ACT_RELU_SQ);
-        }
-    } else if (kind == LIN_DX) {
+        act_all(v, a.act);
+    } else if (a.kind == LIN_DX) {
         if (nv <= 0) return;
         if (a.z || a.z8.codes) {
             float z[8], h[8];
             if (a.z) {
-                load8(a.z, r * a.ld_z + c, dt, FAST || a.z_vec, nv, z);
+                load8(a.z, r * a.ld_z + c, a.dt, a.z_vec, nv, z);
             } else {
                 const float step = act8_step(gm(a.z8.exps)[r * a.z8.lde + c / kAct8Group]);
                 const GMEM int8_t* p = gm(a.z8.codes) + r * a.z8.ld + c;
-                if (FAST || (a.z8.vec && nv >= 8)) {
+                if (a.z8.vec && nv >= 8) {
                     const u32x2_t w = *reinterpret_cast<const GMEM u32x2_t*>(p);
                     act8_dec4(w[0], step, z);
                     act8_dec4(w[1], step, z + 4);
@@ -385,40 +493,35 @@ __device__ __forceinline__ void epilogue8(const LinArgs& a, int64_t r, int64_t c
                     for (int k = 0; k < 8; ++k) z[k] = k < nv ? float(p[k]) * step : 0.f;
                 }
             }
-            float d[8];
-            if (a.act == ACT_GELU) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) act_both(z[k], ACT_GELU, h[k], d[k]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) act_both(z[k], a.act, h[k], d[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= d[k];
-            if (a.act_out) store8(a.act_out, r * a.ld_act + c, dt, FAST || a.act_vec, nv, h);
+            act_grad_all(v, z, h, a.act);
+            if (a.act_out) store8(a.act_out, r * a.ld_act + c, a.dt, a.act_vec, nv, h);
         }
     } else {
         if (nv <= 0) return;
         if (a.accumulate) {
             float o[8];
-            load8(a.out, r * a.ld_out + c, out_dt, FAST || a.out_vec, nv, o);
+            load8(a.out, r * a.ld_out + c, a.out_dt, a.out_vec, nv, o);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] += o[k];
         }
     }
-    if (kind != LIN_DW && a.add) {
+    if (a.kind != LIN_DW && a.add) {
         float b[8];
-        load8(a.add, r * a.ld_add + c, dt, FAST || a.add_vec, nv, b);
+        load8(a.add, r * a.ld_add + c, a.dt, a.add_vec, nv, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += b[k];
     }
-    store8(a.out, r * a.ld_out + c, out_dt, FAST || a.out_vec, nv, v);
+    store8(a.out, r * a.ld_out + c, a.out_dt, a.out_vec, nv, v);
 }
 
-// Every buffer that the epilogue touches allows vectors.
-__device__ __forceinline__ bool vector_epilogue(const LinArgs& a) {
-    return a.out_vec && (!a.bias || a.bias_vec) && (!a.add || a.add_vec) && (!a.z || a.z_vec) &&
-           (!a.z8.codes || a.z8.vec) && (!a.act_out || a.act_vec);
+// Every buffer that the epilogue touches allows vectors, and lane offsets of
+// up to 16 rows fit 32 bits.
+__device__ __forceinline__ bool fast_epilogue(const LinArgs& a) {
+    constexpr int64_t kMost = int64_t(1) << 25;   // 16 rows x 4 bytes x this < 2^32
+    return a.out_vec && a.ld_out <= kMost && (!a.bias || a.bias_vec) && (!a.add || (a.add_vec && a.ld_add <= kMost)) &&
+           (!a.z || (a.z_vec && a.ld_z <= kMost)) &&
+           (!a.z8.codes || (a.z8.vec && a.z8.ld <= kMost && a.z8.lde <= kMost)) &&
+           (!a.act_out || (a.act_vec && a.ld_act <= kMost));
 }
 
 // Shape of the output as stored, and of the split sums (rows padded to whole groups).
@@ -434,12 +537,12 @@ __host__ __device__ inline OutShape out_shape(const LinArgs& a) {
 }
 
 // 8 elements of a split's sums.
-__device__ __forceinline__ void put_partial(const LinArgs& a, const OutShape& o, int split, int64_t r, int64_t c,
+__device__ __forceinline__ void put_partial(const LinArgs& a, const OutShape& o, int split, const RunAt& t,
                                             const float (&v)[8]) {
-    if (r >= o.rows || c >= o.cols) return;   // a run that begins inside may end in the row's padding
-    GMEM float* p = gm(a.partial) + (int64_t(split) * o.rows + r) * o.ldp + c;
+    if (t.r + t.rl >= o.rows || t.c + t.cl >= o.cols) return;   // a run that begins inside may end in the row's padding
+    GMEM char* p = run_ptr(reinterpret_cast<char*>(a.partial) + int64_t(split) * o.rows * o.ldp * 4, o.ldp, t, 4);
     *reinterpret_cast<GMEM f32x4_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<GMEM f32x4_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+    *reinterpret_cast<GMEM f32x4_t*>(p + 16) = f32x4_t{v[4], v[5], v[6], v[7]};
 }
 
 // The output tile (ROWS x COLS at r0, c0, in the output's orientation) lies in
@@ -459,7 +562,7 @@ __device__ __forceinline__ void staged_epilogue(const LinArgs& a, const OutShape
         float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
         int64_t n = o.cols - (c0 + c);
         n = r0 + r < o.rows ? (n > 8 ? 8 : n) : 0;
-        epilogue8<1, -1, false, -1>(a, r0 + r, c0 + c, n > 0 ? int(n) : 0, v);
+        epilogue_any(a, r0 + r, c0 + c, n > 0 ? int(n) : 0, v);
     }
 }
 __device__ __forceinline__ void stage_put(float* stage, int cols, int r, int c, const float (&v)[8]) {
@@ -486,16 +589,17 @@ struct TileAt {
     int split;
     bool in;
 };
-__device__ __forceinline__ TileAt tile_at(const LinArgs& a, int edge) {
-    const int64_t nm = (a.M + edge - 1) / edge, nn = (a.N + edge - 1) / edge, all = nm * nn * a.splits;
-    const int64_t chunk = (all + 7) / 8;
-    const int64_t t = int64_t(blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
+__device__ __forceinline__ TileAt tile_at(const LinArgs& a, int edge) {   // at most 2^31 workgroups
+    const uint32_t nm = uint32_t((a.M + edge - 1) / edge), nn = uint32_t((a.N + edge - 1) / edge), tiles = nm * nn;
+    const uint32_t all = tiles * uint32_t(a.splits), chunk = (all + 7) / 8;
+    const uint32_t t = (blockIdx.x & 7) * chunk + (blockIdx.x >> 3);
     TileAt o;
-    o.in = t < all && int64_t(blockIdx.x >> 3) < chunk;
-    o.split = int(t / (nm * nn));
-    const int64_t u = t % (nm * nn), g = u / (8 * nn), rows = nm - 8 * g < 8 ? nm - 8 * g : 8, w = u % (8 * nn);
-    o.tm = 8 * g + w % rows;
-    o.tn = w / rows;
+    o.in = t < all && (blockIdx.x >> 3) < chunk;
+    const uint32_t split = t / tiles, u = t - split * tiles, g = u / (8 * nn), w = u - g * 8 * nn;
+    const uint32_t rows = nm - 8 * g < 8 ? nm - 8 * g : 8, c = w / rows;
+    o.split = int(split);
+    o.tm = 8 * g + (w - c * rows);
+    o.tn = c;
     return o;
 }
 
@@ -551,11 +655,14 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
 #pragma unroll
         for (int j = 0; j < TI; ++j) fb[j] = frag<T, BKC, W>(st + OPB, wc + 16 * j, s, lane);
     };
-    auto mul = [&](const F(&fa)[TI], const F(&fb)[TI]) {
+    // beside(i): loads issued between the rows' MFMAs
+    auto mul = [&](const F(&fa)[TI], const F(&fb)[TI], auto&& beside) {
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
+        for (int i = 0; i < TI; ++i) {
 #pragma unroll
             for (int j = 0; j < TI; ++j) acc[i][j] = TR ? mma(fa[i], fb[j], acc[i][j]) : mma(fb[j], fa[i], acc[i][j]);
+            beside(i);
+        }
         if (sum_b) {
             const F one = ones<F>();
 #pragma unroll
@@ -584,11 +691,24 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
             F fa0[TI], fb0[TI], fa1[TI], fb1[TI];
             read(smem + stage(0), 0, fa0, fb0);
             for (int kb = 0; kb < nk; ++kb) {
-                issue(kb + NST - 1);     // into the stage of block kb - 1, which every wave has read
+                // Pinned in this order: the compiler would move each read down to
+                // its use.  The loads of block kb + NST - 1 go into the stage of
+                // block kb - 1, which every wave has read: between the MFMAs, or
+                // (eight stages: bound by memory) before them.
+                constexpr bool kFirst = NST == 8;
+                if (kFirst) issue(kb + NST - 1);
                 read(smem + stage(kb), 1, fa1, fb1);
-                mul(fa0, fb0);
+                __builtin_amdgcn_sched_barrier(0);
+                mul(fa0, fb0, [&](int i) {
+                    if (kFirst) return;
+                    const uint32_t st = lds0 + stage(kb + NST - 1);
+                    la.issue(k_of(kb + NST - 1), st, i);
+                    lb.issue(k_of(kb + NST - 1), st + OPB, i);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
                 read(smem + stage(kb + 1), 0, fa0, fb0);
-                mul(fa1, fb1);
+                __builtin_amdgcn_sched_barrier(0);
+                mul(fa1, fb1, [](int) {});
                 vm_wait<kFlight>();      // this wave's part of block kb + 2 has landed
                 __syncthreads();         // and every other wave's
             }
@@ -618,7 +738,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
             for (int s = 0; s < 2; ++s) {
                 F fa[TI], fb[TI];
                 read(smem + at, s, fa, fb);
-                mul(fa, fb);
+                mul(fa, fb, [](int) {});
             }
             if (more) {
                 la.put(smem + into);
@@ -630,7 +750,8 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
     const OutShape o = out_shape(a);
     const int g = lane >> 4, i16 = lane & 15;
     const int64_t r0 = (TR ? t.tn : t.tm) * W, c0 = (TR ? t.tm : t.tn) * W;
-    // f(row, column, values): runs of 8 of this wave's part of the output tile
+    // f(row, column, values): runs of 8 of this wave's part of the output tile; a
+    // lane's own is i16 rows and 8 g columns on
     auto runs = [&](auto&& f) {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
@@ -639,21 +760,21 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
                 float v[8];
                 if constexpr (TR) {
                     join_tiles(acc[2 * p][i], acc[2 * p + 1][i], v);
-                    f(wc + 16 * i + i16, wr + 32 * p + 8 * g, v);
+                    f(wc + 16 * i, wr + 32 * p, v);
                 } else {
                     join_tiles(acc[i][2 * p], acc[i][2 * p + 1], v);
-                    f(wr + 16 * i + i16, wc + 32 * p + 8 * g, v);
+                    f(wr + 16 * i, wc + 32 * p, v);
                 }
             }
     };
     if (a.splits > 1) {
-        runs([&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, r0 + r, c0 + c, v); });
-    } else if (KIND >= 0 && r0 + W <= o.rows && c0 + W <= o.cols && vector_epilogue(a)) {
-        runs([&](int r, int c, float(&v)[8]) { epilogue8<16, KIND, true, N::dt>(a, r0 + r, c0 + c, 8, v); });
+        runs([&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, RunAt{r0 + r, c0 + c, i16, 8 * g}, v); });
+    } else if (KIND >= 0 && r0 + W <= o.rows && c0 + W <= o.cols && fast_epilogue(a)) {
+        runs([&](int r, int c, float(&v)[8]) { epilogue_run<KIND, N::dt>(a, RunAt{r0 + r, c0 + c, i16, 8 * g}, v); });
     } else {
         float* stage = reinterpret_cast<float*>(smem);
         __syncthreads();                 // every wave has read its last fragments
-        runs([&](int r, int c, float(&v)[8]) { stage_put(stage, W, r, c, v); });
+        runs([&](int r, int c, float(&v)[8]) { stage_put(stage, W, r + i16, c + 8 * g, v); });
         __syncthreads();
         staged_epilogue<256>(a, o, stage, W, W, r0, c0);
     }
@@ -916,24 +1037,24 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinArgs a) {
                 float v[8];
                 if constexpr (TR) {      // i: column tile i & 1, row pair i >> 1
                     join_tiles(acc[y][H][2 * (i >> 1)][i & 1], acc[y][H][2 * (i >> 1) + 1][i & 1], v);
-                    f(wc + 16 * (i & 1) + i16, y * 128 + wr + 32 * (i >> 1) + 8 * g, v);
+                    f(wc + 16 * (i & 1), y * 128 + wr + 32 * (i >> 1), v);
                 } else {
                     join_tiles(acc[H][y][i][0], acc[H][y][i][1], v);
-                    f(wr + 16 * i + i16, y * 128 + wc + 8 * g, v);
+                    f(wr + 16 * i, y * 128 + wc, v);
                 }
             }
     };
-    const bool fast = r0 + 256 <= o.rows && c0 + 256 <= o.cols && vector_epilogue(a);
+    const bool fast = r0 + 256 <= o.rows && c0 + 256 <= o.cols && fast_epilogue(a);
     auto half = [&](auto hh) {
         const int64_t rh = r0 + 128 * decltype(hh)::value;
         if (a.splits > 1) {
-            runs(hh, [&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, rh + r, c0 + c, v); });
+            runs(hh, [&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, RunAt{rh + r, c0 + c, i16, 8 * g}, v); });
         } else if (fast) {
-            runs(hh, [&](int r, int c, float(&v)[8]) { epilogue8<16, KIND, true, 0>(a, rh + r, c0 + c, 8, v); });
+            runs(hh, [&](int r, int c, float(&v)[8]) { epilogue_run<KIND, 0>(a, RunAt{rh + r, c0 + c, i16, 8 * g}, v); });
         } else {
             float* stage = reinterpret_cast<float*>(smem);
             __syncthreads();
-            runs(hh, [&](int r, int c, float(&v)[8]) { stage_put(stage, 256, r, c, v); });
+            runs(hh, [&](int r, int c, float(&v)[8]) { stage_put(stage, 256, r + i16, c + 8 * g, v); });
             __syncthreads();
             staged_epilogue<kPpThreads>(a, o, stage, 128, 256, rh, c0);
         }
@@ -986,7 +1107,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int64_t out
             }
         }
     }
-    epilogue8<1, -1, false, -1>(a, r, c, n > 0 ? int(n) : 0, v);
+    epilogue_any(a, r, c, n > 0 ? int(n) : 0, v);
 }
 
 // An operand with rows that are not whole aligned 16-byte chunks, copied into

@@ -26,6 +26,8 @@ inline uint32_t __float_as_uint(float f) { uint32_t u; std::memcpy(&u, &f, 4); r
 inline float emu_exp2(float x) { return std::exp2(x); }
 #define __builtin_amdgcn_exp2f emu_exp2
 #define __builtin_amdgcn_rcpf(x) (1.f / (x))
+inline float emu_med3(float a, float b, float c) { return std::fmax(b, std::fmin(a, c)); }
+#define __builtin_amdgcn_fmed3f emu_med3
 typedef unsigned emu_u2 __attribute__((ext_vector_type(2)));
 #define __builtin_amdgcn_permlane32_swap(a, b, x, y) (emu_u2{(a), (b)})
 #define __builtin_amdgcn_permlane16_swap(a, b, x, y) (emu_u2{(a), (b)})
