@@ -397,7 +397,8 @@ __device__ __forceinline__ void act_grad_all(float (&v)[8], const float (&z)[8],
 
 // The run's 8 elements, all inside, every buffer of the epilogue allowing
 // vectors and 32-bit offsets (fast_epilogue).  The four lanes of a group of 32
-// columns lie 16 apart.
+// columns lie 16 apart, in the same row (so a row past the end leaves them out
+// together).
 template <int KIND, int DT>
 __device__ __forceinline__ void epilogue_run(const LinArgs& a, const RunAt& t, float (&v)[8]) {
     if (KIND == LIN_FWD) {
@@ -547,7 +548,7 @@ __device__ __forceinline__ void put_partial(const LinArgs& a, const OutShape& o,
 
 // The output tile (ROWS x COLS at r0, c0, in the output's orientation) lies in
 // LDS as float32 rows: through the general epilogue, 8 elements a lane.  One
-// copy of its code, for tiles at the edges and buffers without vectors.
+// copy of its code, for tiles past the last column and buffers without vectors.
 __device__ __forceinline__ int stage_at(int cols, int r, int c) {   // float index of 4 elements; chunks XOR row
     return r * cols + (((c >> 2) ^ (r & 15)) << 2);
 }
@@ -769,8 +770,10 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
     };
     if (a.splits > 1) {
         runs([&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, RunAt{r0 + r, c0 + c, i16, 8 * g}, v); });
-    } else if (KIND >= 0 && r0 + W <= o.rows && c0 + W <= o.cols && fast_epilogue(a)) {
-        runs([&](int r, int c, float(&v)[8]) { epilogue_run<KIND, N::dt>(a, RunAt{r0 + r, c0 + c, i16, 8 * g}, v); });
+    } else if (KIND >= 0 && c0 + W <= o.cols && fast_epilogue(a)) {
+        runs([&](int r, int c, float(&v)[8]) {
+            if (r0 + r + i16 < o.rows) epilogue_run<KIND, N::dt>(a, RunAt{r0 + r, c0 + c, i16, 8 * g}, v);
+        });
     } else {
         float* stage = reinterpret_cast<float*>(smem);
         __syncthreads();                 // every wave has read its last fragments
@@ -1044,13 +1047,15 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(LinArgs a) {
                 }
             }
     };
-    const bool fast = r0 + 256 <= o.rows && c0 + 256 <= o.cols && fast_epilogue(a);
+    const bool fast = c0 + 256 <= o.cols && fast_epilogue(a);
     auto half = [&](auto hh) {
         const int64_t rh = r0 + 128 * decltype(hh)::value;
         if (a.splits > 1) {
             runs(hh, [&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, RunAt{rh + r, c0 + c, i16, 8 * g}, v); });
         } else if (fast) {
-            runs(hh, [&](int r, int c, float(&v)[8]) { epilogue_run<KIND, 0>(a, RunAt{rh + r, c0 + c, i16, 8 * g}, v); });
+            runs(hh, [&](int r, int c, float(&v)[8]) {
+                if (rh + r + i16 < o.rows) epilogue_run<KIND, 0>(a, RunAt{rh + r, c0 + c, i16, 8 * g}, v);
+            });
         } else {
             float* stage = reinterpret_cast<float*>(smem);
             __syncthreads();
