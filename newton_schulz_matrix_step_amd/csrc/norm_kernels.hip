@@ -306,13 +306,14 @@ __global__ __launch_bounds__(kNT) void norm_long_kernel(NormArgs a) {
 // Backward.  A workgroup walks rows with a stride of the grid and keeps, per
 // lane, the running sums of dy xh and dy of its columns; at the end it adds the
 // sums of its row groups in LDS and writes one row of partial sums.  A second
-// kernel adds the partial rows in a fixed order.
+// kernel adds the partial rows in a fixed order.  Few workgroups (one a CU): each
+// costs a row of partial sums written and read again.
 template <class T, bool VEC, int NW, int E>
 __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGradArgs a) {
     using G = RowGeom<T, VEC, NW, E>;
     constexpr int RB = kWaves / NW;
     __shared__ float red[2][kWaves][2];
-    __shared__ float cs[RB > 1 ? 2 * G::LANES * E : 1];
+    __shared__ float cs[RB > 1 ? 2 * kNT * E : 1];   // [row group][sum][element][lane]
     const int wave = threadIdx.x >> 6, lane = threadIdx.x % G::LANES, rg = wave / NW;
     float g[E], dg[E], db[E];
     param_load<T, VEC, NW, E>(a.gain, a.pdt, a.pvec, a.cols, lane, g);
@@ -320,19 +321,18 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGradArgs a) {
     for (int i = 0; i < E; ++i) dg[i] = db[i] = 0.f;
     const float n = float(a.cols);   // divided by: the mean of equal values is exact
     const int64_t step = int64_t(gridDim.x) * RB;
-    RowRaw<T, VEC, NW, E> rx, ry;
+    RowRaw<T, VEC, NW, E> rx, ry, ra;
     int64_t r0 = int64_t(blockIdx.x) * RB;
     if (r0 < a.rows) {
         row_load<T, VEC, NW, E>(a.x, (r0 + rg) * a.ld_x, a.cols, lane, r0 + rg < a.rows, rx);
         row_load<T, VEC, NW, E>(a.dy, (r0 + rg) * a.ld_dy, a.cols, lane, r0 + rg < a.rows, ry);
+        if (a.add) row_load<T, VEC, NW, E>(a.add, (r0 + rg) * a.ld_add, a.cols, lane, r0 + rg < a.rows, ra);
     }
     int half = 0;
     for (; r0 < a.rows; r0 += step, half ^= 1) {
         const int64_t row = r0 + rg;
         const bool on = row < a.rows;
         const float mu = on ? gm(a.mean)[row] : 0.f, r = on ? gm(a.rstd)[row] : 0.f;
-        RowRaw<T, VEC, NW, E> ra;
-        if (a.add) row_load<T, VEC, NW, E>(a.add, row * a.ld_add, a.cols, lane, on, ra);
         float xh[E], y[E];
         row_decode<T, VEC, NW, E>(rx, xh);
         row_decode<T, VEC, NW, E>(ry, y);
@@ -358,39 +358,48 @@ __global__ __launch_bounds__(kNT) void norm_grad_kernel(NormGradArgs a) {
             row_decode<T, VEC, NW, E>(ra, xh);
 #pragma unroll
             for (int i = 0; i < E; ++i) y[i] += xh[i];
+            // (add may be dx: another row's, not yet written)
+            row_load<T, VEC, NW, E>(a.add, nr * a.ld_add, a.cols, lane, nr < a.rows, ra);
         }
         if (on) row_store<T, VEC, NW, E>(a.dx, row * a.ld_dx, a.cols, lane, y);
     }
-    if constexpr (RB > 1) {
-        for (int w = 0; w < RB; ++w) {
-            if (rg == w) {
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    float* p = cs + i * G::LANES + lane;
-                    float* q = p + G::LANES * E;
-                    *p = w ? *p + dg[i] : dg[i];
-                    *q = w ? *q + db[i] : db[i];
-                }
-            }
-            __syncthreads();
-        }
-        if (rg != 0) return;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            dg[i] = cs[i * G::LANES + lane];
-            db[i] = cs[(E + i) * G::LANES + lane];
-        }
-    }
     GMEM float* pg = gm(a.partial) + int64_t(blockIdx.x) * a.cols;
     GMEM float* pb = pg + int64_t(a.parts) * a.cols;
+    if constexpr (RB > 1) {
+        // every row group's sums through LDS, each thread adding its share of the columns
+        constexpr int kOne = G::LANES * E;
 #pragma unroll
-    for (int j = 0; j < G::C; ++j) {
-        const int c = G::col(j, lane);
-        if (c >= a.cols) continue;
+        for (int i = 0; i < E; ++i) {
+            cs[(rg * 2 * E + i) * G::LANES + lane] = dg[i];
+            cs[((rg * 2 + 1) * E + i) * G::LANES + lane] = db[i];
+        }
+        __syncthreads();
 #pragma unroll
-        for (int k = 0; k < G::V; ++k) {
-            pg[c + k] = dg[j * G::V + k];
-            pb[c + k] = db[j * G::V + k];
+        for (int q = 0; q < 2 * kOne / kNT; ++q) {
+            const int at = q * kNT + threadIdx.x, w = at / kOne, i = at % kOne / G::LANES, l = at % G::LANES;
+            float v = 0.f;
+#pragma unroll
+            for (int r = 0; r < RB; ++r) v += cs[r * 2 * kOne + at];
+            const int c = G::col(i / G::V, l) + i % G::V;
+            if (c < a.cols) (w ? pb : pg)[c] = v;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < G::C; ++j) {
+            const int c = G::col(j, lane);
+            if (c >= a.cols) continue;
+            if constexpr (VEC) {         // cols is a multiple of V: 16-byte aligned rows
+#pragma unroll
+                for (int k = 0; k < G::V; k += 4) {
+                    const float* x = dg + j * G::V + k;
+                    const float* y = db + j * G::V + k;
+                    *reinterpret_cast<GMEM f32x4_t*>(pg + c + k) = f32x4_t{x[0], x[1], x[2], x[3]};
+                    *reinterpret_cast<GMEM f32x4_t*>(pb + c + k) = f32x4_t{y[0], y[1], y[2], y[3]};
+                }
+            } else {
+                pg[c] = dg[j];
+                pb[c] = db[j];
+            }
         }
     }
 }
@@ -437,9 +446,11 @@ __global__ __launch_bounds__(kNT) void norm_grad_join_kernel(NormGradArgs a) {
     const int c = blockIdx.x * kRedCols + cl;
     const int which = blockIdx.y;
     float s = 0.f;
-    if (c < a.cols)
-        for (int p = pl; p < a.parts; p += kNT / kRedCols)
-            s += gm(a.partial)[(int64_t(which) * a.parts + p) * a.cols + c];
+    if (c < a.cols) {
+        const GMEM float* q = gm(a.partial) + int64_t(which) * a.parts * a.cols + c;
+#pragma unroll 8
+        for (int p = pl; p < a.parts; p += kNT / kRedCols) s += q[int64_t(p) * a.cols];
+    }
     acc[threadIdx.x] = s;
     __syncthreads();
     if (pl != 0 || c >= a.cols) return;
@@ -521,7 +532,9 @@ bool pick_row(int cols, F&& f) {
 }
 int row_waves(int cols) { return cols <= 1024 ? 1 : cols <= 2048 ? 2 : cols <= 4096 ? 4 : 8; }
 
-constexpr int kMaxFwdBlocks = 1024;
+// Forward: two workgroups a CU (8192 x 4096 bf16 27.5 us; four a CU 29.4).
+// Backward: one (45.8 us; half as many 64.5, half as many again 58).
+constexpr int kMaxFwdBlocks = 512;
 constexpr int kMaxGradParts = 256;
 
 }  // namespace
