@@ -180,7 +180,7 @@ typedef struct muon_adamw_hparams {
  * element is off by at most half a step, 2^-7 of its group's largest magnitude
  * (2^-8 at best).  Decoding is exact in bfloat16 and float32.  A group holding
  * an infinity or a NaN gets exponent byte 255 and codes 0: all of it decodes to
- * NaN. */
+ * NaN.  The encoder writes bytes 1..249 and 255; byte 0 decodes to zeros. */
 typedef struct muon_act8 {
     int8_t  *codes;            /* rows x cols */
     uint8_t *exponents;        /* rows x ceil(cols / 32) */

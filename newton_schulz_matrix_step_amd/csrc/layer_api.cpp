@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
@@ -173,11 +174,11 @@ struct Check {   // collects the first complaint
         need(static_cast<const void*>(q.codes) != static_cast<const void*>(q.exponents), "%s: codes alias exponents", what);
     }
     // no output may be an input or another output
-    void distinct(const std::vector<const void*>& outs, const std::vector<const void*>& ins) {
-        for (size_t i = 0; i < outs.size(); ++i) {
-            if (!outs[i]) continue;
-            for (size_t j = i + 1; j < outs.size(); ++j) need(outs[i] != outs[j], "two outputs alias");
-            for (const void* in : ins) need(outs[i] != in, "an output aliases an input");
+    void distinct(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+        for (auto o = outs.begin(); o != outs.end(); ++o) {
+            if (!*o) continue;
+            for (auto p = o + 1; p != outs.end(); ++p) need(*o != *p, "two outputs alias");
+            for (const void* in : ins) need(*o != in, "an output aliases an input");
         }
     }
 };
@@ -235,9 +236,9 @@ muon_status run_linear(HandleBase* h, LinArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-extern "C" {
+namespace {
 
-muon_status muon_layernorm_forward(muon_handle* handle, const muon_layernorm_args* args, void* stream) {
+muon_status layernorm_forward(muon_handle* handle, const muon_layernorm_args* args, void* stream) {
     LAYER_ENTER(handle, args);
     const muon_layernorm_args& p = *args;
     ck.dtype(p.dtype, "x");
@@ -284,7 +285,7 @@ muon_status muon_layernorm_forward(muon_handle* handle, const muon_layernorm_arg
     return MUON_OK;
 }
 
-muon_status muon_layernorm_backward(muon_handle* handle, const muon_layernorm_grad_args* args, void* stream) {
+muon_status layernorm_backward(muon_handle* handle, const muon_layernorm_grad_args* args, void* stream) {
     LAYER_ENTER(handle, args);
     const muon_layernorm_grad_args& p = *args;
     ck.dtype(p.dtype, "x");
@@ -343,7 +344,7 @@ muon_status muon_layernorm_backward(muon_handle* handle, const muon_layernorm_gr
     return MUON_OK;
 }
 
-muon_status muon_linear_forward(muon_handle* handle, const muon_linear_args* args, void* stream) {
+muon_status linear_forward(muon_handle* handle, const muon_linear_args* args, void* stream) {
     LAYER_ENTER(handle, args);
     const muon_linear_args& p = *args;
     ck.dtype(p.dtype, "x");
@@ -404,7 +405,7 @@ muon_status muon_linear_forward(muon_handle* handle, const muon_linear_args* arg
     return run_linear(h, a, static_cast<hipStream_t>(stream));
 }
 
-muon_status muon_linear_grad_input(muon_handle* handle, const muon_linear_grad_input_args* args, void* stream) {
+muon_status linear_grad_input(muon_handle* handle, const muon_linear_grad_input_args* args, void* stream) {
     LAYER_ENTER(handle, args);
     const muon_linear_grad_input_args& p = *args;
     ck.dtype(p.dtype, "dy");
@@ -466,7 +467,7 @@ muon_status muon_linear_grad_input(muon_handle* handle, const muon_linear_grad_i
     return run_linear(h, a, static_cast<hipStream_t>(stream));
 }
 
-muon_status muon_linear_grad_weight(muon_handle* handle, const muon_linear_grad_weight_args* args, void* stream) {
+muon_status linear_grad_weight(muon_handle* handle, const muon_linear_grad_weight_args* args, void* stream) {
     LAYER_ENTER(handle, args);
     const muon_linear_grad_weight_args& p = *args;
     ck.dtype(p.dtype, "dy");
@@ -518,8 +519,6 @@ muon_status muon_linear_grad_weight(muon_handle* handle, const muon_linear_grad_
     return run_linear(h, a, static_cast<hipStream_t>(stream));
 }
 
-namespace {
-
 muon_status run_act8(HandleBase* h, Act8Args& a, const muon_act8& q, const void* m, int64_t cols, int32_t dtype,
                      bool encode, hipStream_t stream) {
     a.q = act8_view(q);
@@ -533,9 +532,7 @@ muon_status run_act8(HandleBase* h, Act8Args& a, const muon_act8& q, const void*
     return MUON_OK;
 }
 
-}  // namespace
-
-muon_status muon_act_encode(muon_handle* handle, const void* x, int64_t rows, int64_t cols, int64_t ld_x, int32_t dtype,
+muon_status act_encode(muon_handle* handle, const void* x, int64_t rows, int64_t cols, int64_t ld_x, int32_t dtype,
                             const muon_act8* q, void* stream) {
     LAYER_ENTER(handle, q);
     ck.dtype(dtype, "x");
@@ -555,7 +552,7 @@ muon_status muon_act_encode(muon_handle* handle, const void* x, int64_t rows, in
     return run_act8(h, a, *q, x, cols, dtype, true, static_cast<hipStream_t>(stream));
 }
 
-muon_status muon_act_decode(muon_handle* handle, const muon_act8* q, void* y, int64_t rows, int64_t cols, int64_t ld_y,
+muon_status act_decode(muon_handle* handle, const muon_act8* q, void* y, int64_t rows, int64_t cols, int64_t ld_y,
                             int32_t dtype, void* stream) {
     LAYER_ENTER(handle, q);
     ck.dtype(dtype, "y");
@@ -573,6 +570,44 @@ muon_status muon_act_decode(muon_handle* handle, const muon_act8* q, void* y, in
     a.rows = rows;
     a.ld = ld_y;
     return run_act8(h, a, *q, y, cols, dtype, false, static_cast<hipStream_t>(stream));
+}
+
+// No exception (an allocation of the host's that fails) leaves a C entry.
+template <class F>
+muon_status guarded(F&& f) noexcept {
+    try {
+        return f();
+    } catch (...) {
+        return MUON_ERR_OOM;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_layernorm_forward(muon_handle* h, const muon_layernorm_args* args, void* stream) {
+    return guarded([&] { return layernorm_forward(h, args, stream); });
+}
+muon_status muon_layernorm_backward(muon_handle* h, const muon_layernorm_grad_args* args, void* stream) {
+    return guarded([&] { return layernorm_backward(h, args, stream); });
+}
+muon_status muon_linear_forward(muon_handle* h, const muon_linear_args* args, void* stream) {
+    return guarded([&] { return linear_forward(h, args, stream); });
+}
+muon_status muon_linear_grad_input(muon_handle* h, const muon_linear_grad_input_args* args, void* stream) {
+    return guarded([&] { return linear_grad_input(h, args, stream); });
+}
+muon_status muon_linear_grad_weight(muon_handle* h, const muon_linear_grad_weight_args* args, void* stream) {
+    return guarded([&] { return linear_grad_weight(h, args, stream); });
+}
+muon_status muon_act_encode(muon_handle* h, const void* x, int64_t rows, int64_t cols, int64_t ld_x, int32_t dtype,
+                            const muon_act8* q, void* stream) {
+    return guarded([&] { return act_encode(h, x, rows, cols, ld_x, dtype, q, stream); });
+}
+muon_status muon_act_decode(muon_handle* h, const muon_act8* q, void* y, int64_t rows, int64_t cols, int64_t ld_y,
+                            int32_t dtype, void* stream) {
+    return guarded([&] { return act_decode(h, q, y, rows, cols, ld_y, dtype, stream); });
 }
 
 }  // extern "C"

@@ -1233,6 +1233,11 @@ hipError_t launch_typed(const LinArgs& a, hipStream_t s) {
 // whole aligned chunks are read element by element by the product, about nine
 // times slower per k block, or copied first to rows that have them (4000 x 3001
 // -> 2047: 480 and 89 us; 1 x 2001 -> 999: 14 and 17).
+// MUON_LINEAR_EDGE fixes the edge where that tile can serve the call (a host
+// build for bounds checking runs each kernel on small sizes); 0: by the model.
+#ifndef MUON_LINEAR_EDGE
+#define MUON_LINEAR_EDGE 0
+#endif
 struct TileCost {
     int edge;
     double fixed, block, block_dw, block_f32;
@@ -1276,6 +1281,7 @@ LinPlan plan_linear(const LinArgs& a) {
                 us = std::max(us, bytes_us);
                 if (s > 1) us += 4 + double(s) * double(o.rows) * double(o.ldp) * 8 / 5e6;
                 us += relay_us;
+                if (MUON_LINEAR_EDGE && tc.edge != MUON_LINEAR_EDGE) us += 1e9;
                 if (us < best_us) {
                     best_us = us;
                     best.tile = tc.edge;

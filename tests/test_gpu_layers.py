@@ -389,6 +389,57 @@ def test_linear_grad_weight(nsm, h, rows, k, n, layout, st):
         assert padding_kept(dw)
 
 
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("rows,k,n", [(2050, 2048, 1408), (4090, 1024, 4104), (8192, 1000, 2048), (3000, 2051, 1999)])
+def test_linear_large_products(nsm, h, rows, k, n, layout):
+    """Sizes that take the wider tiles, splits and re-laid operands (ragged rows
+    and columns, odd leading dimensions), bf16, against float64 products on the
+    GPU; the bounds as above."""
+    import torch
+    bf = torch.bfloat16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows + k)
+
+    def rnd(*s, std=1.0):
+        return torch.empty(*s, device="cuda").normal_(0, std, generator=g).to(bf)
+
+    def near(got, want, tol, what):
+        bad = (got.double() - want).abs() > tol
+        assert not bool(bad.any()), f"{what}: {int(bad.sum())} off, first at {bad.nonzero()[0].tolist()}"
+
+    def decoded(q):
+        step = torch.exp2(q.exponents.double() - 127)
+        return q.codes.double() * step.repeat_interleave(32, dim=1)[:, :q.codes.shape[1]]
+
+    x, b, res, dy = rnd(rows, k), rnd(n), rnd(rows, n), rnd(rows, n)
+    w = rnd(*((n, k) if layout == "out_in" else (k, n)), std=k ** -0.5)
+    wio = (w.t() if layout == "out_in" else w).double()
+    y, z8 = torch.empty_like(res), nsm.Act8.empty(rows, n)
+    nsm.muon_linear_forward(h, x, w, y, bias=b, act="gelu", residual=res, z_out=z8, w_layout=layout)
+    z = x.double() @ wio + b.double()
+    mag = x.double().abs() @ wio.abs() + b.double().abs()
+    ry = torch.nn.functional.gelu(z, approximate="tanh") + res.double()
+    near(y, ry, (k + 16) * U * 1.2 * mag + 8 * U * (1 + ry.abs()) + 2 * U * res.double().abs() + (4 * U + 2.0 ** -8) * ry.abs(), "y")
+    step = torch.exp2(z8.exponents.double() - 127).repeat_interleave(32, dim=1)[:, :n]
+    near(decoded(z8), z, step / 2 + (k + 16) * U * mag, "z8")
+    # through the activation of this layer's own pre-activation sizes: z is rows x k
+    zi = nsm.Act8.empty(rows, k)
+    nsm.muon_act_encode(h, x, zi)
+    dx, v = torch.empty_like(x), torch.empty_like(x)
+    nsm.muon_linear_grad_input(h, dy, w, dx, act="relu_sq", z=zi, act_out=v, w_layout=layout)
+    zd = decoded(zi).clamp_min(0)
+    rdx = (dy.double() @ wio.t()) * 2 * zd
+    near(dx, rdx, (n + 16) * U * (dy.double().abs() @ wio.abs().t()) * 2 * zd + (32 * U + 2.0 ** -8) * rdx.abs(), "dx")
+    near(v, zd * zd, (4 * U + 2.0 ** -8) * zd * zd, "act_out")
+    for xin, xv, dt in ((x, x.double(), bf), (zi, decoded(zi), torch.float32)):
+        dw, db = torch.empty(w.shape, device="cuda", dtype=dt), torch.empty(n, device="cuda")
+        nsm.muon_linear_grad_weight(h, xin, dy, dw, db=db, w_layout=layout)
+        rdw, m = xv.t() @ dy.double(), xv.abs().t() @ dy.double().abs()
+        got = dw.t() if layout == "out_in" else dw
+        near(got, rdw, (rows + 16) * U * m + (4 * U + (2.0 ** -8 if dt is bf else 2.0 ** -24)) * rdw.abs(), "dw")
+        near(db, dy.double().sum(0), (rows + 16) * U * dy.double().abs().sum(0), "db")
+
+
 def test_linear_no_rows(nsm, h):
     import torch
     bf = torch.bfloat16

@@ -15,14 +15,13 @@ EMU = os.path.join(ROOT, "tests", "emu_layers")
 CXX = "/opt/rocm/lib/llvm/bin/clang++"
 
 
-@pytest.fixture(scope="module")
-def emu(tmp_path_factory):
+def _build(tmp_path_factory, name, extra):
     if not os.path.exists(CXX):
         pytest.skip("ROCm clang++ not available")
-    out = tmp_path_factory.mktemp("emu_layers")
+    out = tmp_path_factory.mktemp(name)
     flags = ["-O1", "-g", "-std=c++17", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
              "-fno-omit-frame-pointer", f"-I{EMU}", f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}",
-             "-Wno-unused-value"]
+             "-Wno-unused-value", *extra]
     jobs = []
     for src in ("muon_kernels.hip", "adamw_kernels.hip", "muon_static.hip", "norm_kernels.hip", "linear_kernels.hip",
                 "muon_api.cpp", "layer_api.cpp"):
@@ -35,6 +34,11 @@ def emu(tmp_path_factory):
     exe = str(out / "emu_layers_driver")
     subprocess.run([CXX, "-fsanitize=address,undefined", *[o for o, _ in jobs], "-o", exe], check=True)
     return exe
+
+
+@pytest.fixture(scope="module")
+def emu(tmp_path_factory):
+    return _build(tmp_path_factory, "emu_layers", [])
 
 
 # op, rows, cols / in, out, dtype (0 bf16, 1 f32), flags (1 out x in, 2 8-bit, 4 no optional arguments), pad, shift
@@ -71,6 +75,24 @@ def test_layer_kernels_stay_in_bounds(emu, op):
                 _run(emu, case)
             except AssertionError as e:
                 raise AssertionError(f"{case}: {e}") from e
+
+
+# The 128- and 256-wide kernels, which the library gives only to larger products.
+EDGE_CASES = [("lin", r, i, o, dt, fl, pad, sh)
+              for r, i, o in ((1, 8, 8), (130, 200, 264), (257, 136, 300), (300, 1000, 520))
+              for dt, fl, pad, sh in ((0, 0, 0, 0), (0, 1, 8, 0), (0, 2, 0, 0), (0, 3, 0, 0), (0, 7, 3, 1), (1, 3, 0, 0))]
+
+
+@pytest.mark.parametrize("edge,kernel", [(128, "linear_tile_kernel"), (256, "linear_pp_kernel")])
+def test_wider_tiles_stay_in_bounds(tmp_path_factory, edge, kernel):
+    exe = _build(tmp_path_factory, f"emu_layers_{edge}", [f"-DMUON_LINEAR_EDGE={edge}"])
+    seen = ""
+    for case in EDGE_CASES:
+        try:
+            seen += _run(exe, case, verbose=True).stderr
+        except AssertionError as e:
+            raise AssertionError(f"{case}: {e}") from e
+    assert kernel in seen
 
 
 def test_refusals_enqueue_nothing(emu):
