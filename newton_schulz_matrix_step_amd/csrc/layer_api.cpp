@@ -43,15 +43,20 @@ muon_status hip_fail(HandleBase* h, hipError_t e, const char* what) {
     return fail(h, MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+// The handle's device for a scope; the calls are short, so a device that is
+// current already is left alone.
 struct DeviceGuard {
     int old = -1;
-    bool ok = false;
+    bool ok = true, set = false;
     explicit DeviceGuard(int dev) {
         if (hipGetDevice(&old) != hipSuccess) old = -1;
-        ok = hipSetDevice(dev) == hipSuccess;
+        if (old != dev) {
+            set = true;
+            ok = hipSetDevice(dev) == hipSuccess;
+        }
     }
     ~DeviceGuard() {
-        if (old >= 0) (void)hipSetDevice(old);
+        if (set && old >= 0) (void)hipSetDevice(old);
     }
 };
 
@@ -464,6 +469,11 @@ muon_status linear_grad_input(muon_handle* handle, const muon_linear_grad_input_
     a.act_out = p.act_out;
     a.ld_act = p.ld_act_out;
     a.act_vec = p.act_out && rows_vec(p.act_out, p.ld_act_out, p.dtype);
+    // dx and act_out together past what the L2s hold (32 MiB): the lines of one
+    // are sent out as they are written, not at the kernel's end (4001 x 1024,
+    // weight 4096 x 1024, 2 x 31 MiB written: 58.1 -> 47.4 us; both streamed
+    // 45.4, but the products that read dx next lose more than that).
+    a.act_stream = p.act_out && 2 * p.rows * p.in * es > (32ll << 20);
     return run_linear(h, a, static_cast<hipStream_t>(stream));
 }
 

@@ -63,6 +63,14 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int dt, bool vec
     for (int k = 0; k < 8; ++k) v[k] = k < n ? load1(p, i + k, dt) : 0.f;
 }
 
+// 16 bytes; STREAM: past the caches where that can be (each XCD's L2 writes its
+// dirty lines back at the kernel's end, and a streamed line has left by then).
+template <bool STREAM, class V>
+__device__ __forceinline__ void put16(GMEM void* p, V w) {
+    GMEM V* q = reinterpret_cast<GMEM V*>(p);
+    if constexpr (STREAM) __builtin_nontemporal_store(w, q);
+    else *q = w;
+}
 __device__ __forceinline__ void store8(void* p, int64_t i, int dt, bool vec, int n, const float (&v)[8]) {
     if (vec && n >= 8) {
         if (dt == 0) {

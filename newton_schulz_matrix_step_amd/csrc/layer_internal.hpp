@@ -121,6 +121,7 @@ struct LinArgs {
     void* act_out;             // M x N: act(z) (LIN_DX)
     int64_t ld_act;
     int32_t act_vec;
+    int32_t act_stream;        // act_out is stored past the L2s
     void* db;                  // N: column sums of B (LIN_DW), may be null
     int32_t db_dt;
     // split of the k range over workgroups: each writes its sums to `partial`

@@ -346,16 +346,16 @@ __device__ __forceinline__ void run_load(const void* p, int64_t ld, const RunAt&
         }
     }
 }
-template <int DT>
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ void run_store(void* p, int64_t ld, const RunAt& t, int dt_arg, const float (&v)[8]) {
     const int dt = DT >= 0 ? DT : dt_arg;
     GMEM char* q = run_ptr(static_cast<char*>(p), ld, t, dt == 0 ? 2 : 4);
     if (dt == 0) {
-        *reinterpret_cast<GMEM u32x4_t*>(q) =
-            u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+        put16<STREAM>(q, u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                 pack_bf16(v[6], v[7])});
     } else {
-        *reinterpret_cast<GMEM f32x4_t*>(q) = f32x4_t{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<GMEM f32x4_t*>(q + 16) = f32x4_t{v[4], v[5], v[6], v[7]};
+        put16<STREAM>(q, f32x4_t{v[0], v[1], v[2], v[3]});
+        put16<STREAM>(q + 16, f32x4_t{v[4], v[5], v[6], v[7]});
     }
 }
 template <int SH>
@@ -431,7 +431,15 @@ __device__ __forceinline__ void epilogue_run(const LinArgs& a, const RunAt& t, f
                 act8_dec4(w[1], step, z + 4);
             }
             act_grad_all(v, z, h, a.act);
-            if (a.act_out) run_store<DT>(a.act_out, a.ld_act, t, DT, h);
+            if (a.act_out) {
+                if (a.act_stream) {
+                    asm volatile("");    // or both stores become one that does not stream
+                    run_store<DT, true>(a.act_out, a.ld_act, t, DT, h);
+                    asm volatile("");
+                } else {
+                    run_store<DT>(a.act_out, a.ld_act, t, DT, h);
+                }
+            }
         }
     } else if (a.accumulate) {
         float o[8];

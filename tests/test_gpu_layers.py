@@ -356,6 +356,23 @@ def test_linear_grad_input(nsm, h, rows, k, n, layout, st):
         assert padding_kept(dx)
 
 
+@pytest.mark.parametrize("rows,k,n,layout", [(2101, 4096, 40, "in_out"), (2048, 4224, 64, "out_in")])
+def test_linear_grad_input_large_outputs(nsm, h, rows, k, n, layout):
+    """dx and act(z) together larger than the caches they are kept in."""
+    rng = np.random.default_rng([28, rows, k, n])
+    dy, dyv = dev(rng.standard_normal((rows, n)), "bf16")
+    w, wv = dev(rng.standard_normal((n, k) if layout == "out_in" else (k, n)) / np.sqrt(n), "bf16")
+    z, zv = act8_dev(nsm, rng.standard_normal((rows, k)) * 3)
+    dx, v = blank(rows, k, "bf16"), blank(rows, k, "bf16")
+    nsm.muon_linear_grad_input(h, dy, w, dx, act="gelu", z=z, act_out=v, w_layout=layout)
+    rdx, rv = lo.linear_grad_input(dyv, wv, "gelu", zv, None, layout)
+    wio = lo.weight_in_out(wv, layout).T
+    der = np.abs(lo.activation(zv, "gelu")[1])
+    tol = lin_tol(n, np.abs(dyv) @ np.abs(wio), der, rdx, "bf16") + 16 * U * np.abs(dyv @ wio)
+    close(host(dx), rdx, tol, "dx")
+    close(host(v), rv, 8 * U * (1 + np.abs(rv)) + HALF["bf16"] * np.abs(rv), "act_out")
+
+
 DW_SHAPES = [(1, 1, 1), (1, 8, 16), (5, 40, 72), (33, 131, 67), (64, 128, 128), (100, 200, 264), (257, 256, 136),
              (1000, 96, 520), (4100, 72, 40), (513, 1408, 264), (1300, 1001, 771)]
 
