@@ -471,7 +471,9 @@ __global__ __launch_bounds__(kNT) void norm_grad_join_kernel(NormGradArgs a) {
 }
 
 // ---- 8-bit checkpoints: 8 elements a lane, 4 lanes a group ----
-// A workgroup takes RPB rows of `slots` 8-element runs each (padded to whole groups).
+// A workgroup takes RPB rows of `slots` 8-element runs each (padded to whole
+// groups).  HBM bound: 16384 x 4096 bf16 encoded and decoded in 79-80 us, 406 MB
+// at 5.1 TB/s.
 __global__ __launch_bounds__(256) void act8_encode_kernel(Act8Args a, int rpb, int slots) {
     const int64_t r0 = int64_t(blockIdx.x) * rpb;
     const int n = rpb * slots;           // multiple of 4; every lane of a group runs the same steps
