@@ -191,7 +191,8 @@ typedef struct muon_act8 {
 
 typedef enum muon_activation {
     MUON_ACT_NONE = 0,
-    MUON_ACT_GELU = 1,         /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    MUON_ACT_GELU = 1,         /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)));
+                                  at infinite z the limits: 0 and infinity, derivatives 0 and 1 */
     MUON_ACT_RELU_SQ = 2       /* max(z, 0)^2 */
 } muon_activation;
 
