@@ -401,8 +401,9 @@ muon_status muon_adamw_step(muon_handle *h, const muon_adamw_tensor *tensors, in
  * Conventions of the seven layer operators: every matrix is row-major with a
  * leading dimension in elements; any alignment of the element type and any
  * size is taken (16-byte aligned rows of whole 16-byte chunks run fastest);
- * rows == 0 enqueues nothing, except that the gradients of parameters are then
- * zeroed (or left, with accumulate).  Nothing but the named outputs is
+ * rows == 0 enqueues nothing (every matrix with a row per token may then be
+ * NULL), except that the gradients of parameters are zeroed (or left, with
+ * accumulate).  Nothing but the named outputs is
  * written: a leading dimension's padding keeps its values.  Outputs may not be
  * inputs or each other except where noted (base addresses are compared).
  * Results do not depend on timing: the same call gives the same bits.  They

@@ -431,8 +431,9 @@ muon_status linear_grad_input(muon_handle* handle, const muon_linear_grad_input_
     ck.matrix(p.act_out, p.ld_act_out, p.in, p.dtype, "act_out");
     ck.act8(p.z8, p.in, "z8");
     ck.need(!(p.z && p.z8.codes), "both z and z8");
-    ck.need(has_z || !p.act_out, "act_out without z or z8");
-    ck.need(has_z || p.activation == MUON_ACT_NONE, "an activation without z or z8");
+    const bool z_known = has_z || p.rows == 0;   // an empty tensor's address is null
+    ck.need(z_known || !p.act_out, "act_out without z or z8");
+    ck.need(z_known || p.activation == MUON_ACT_NONE, "an activation without z or z8");
     ck.need(!p.add || p.add != p.dx || p.ld_add == p.ld_dx, "add is dx with another leading dimension");
     ck.distinct({p.dx, p.act_out},
                 {p.dy, p.w, p.z, p.z8.codes, p.z8.exponents, p.add == p.dx ? nullptr : p.add});
