@@ -407,13 +407,16 @@ muon_status muon_adamw_step(muon_handle *h, const muon_adamw_tensor *tensors, in
  * written: a leading dimension's padding keeps its values.  Outputs may not be
  * inputs or each other except where noted (base addresses are compared).
  * Results do not depend on timing: the same call gives the same bits.  They
- * are not among the profiled roles.  Workspaces belong to the handle, grow to
- * what the largest call needs and are kept until muon_destroy; calls on one
- * handle share them and must be ordered, like those of muon_step.  A call
- * captured into a HIP graph must find its workspace large enough, so a call of
- * the same sizes must have run once outside capture (MUON_ERR_INVALID_ARG
- * otherwise); a workspace that a graph uses is never freed or moved while the
- * handle lives.  Errors: MUON_ERR_INVALID_ARG (a null handle, argument struct
+ * are not among the profiled roles.  Workspaces belong to the handle and grow
+ * in blocks, each at least twice the one before (of the size needed where that
+ * cannot be had), of which none is freed or moved until muon_destroy, as a
+ * graph may use it: doubled blocks together hold less than four times what the
+ * largest call needs.  Calls on one handle share them and
+ * must be ordered, like those of muon_step (graphs captured from one handle
+ * too, when they are replayed).  A call captured into a HIP graph must find its
+ * workspace large enough, so a call of the same sizes, leading dimensions and
+ * alignments must have run once outside capture (MUON_ERR_INVALID_ARG
+ * otherwise).  Errors: MUON_ERR_INVALID_ARG (a null handle, argument struct
  * or required pointer, a size or leading dimension out of range, aliasing, an
  * unknown activation or weight layout, both z and z8, act_out without either, an
  * activation without either in muon_linear_grad_input, flags other than 0 and
@@ -459,7 +462,8 @@ int32_t muon_kernel_stats_read(muon_handle *h, muon_kernel_stats *out, int32_t m
 void muon_kernel_stats_reset(muon_handle *h);
 
 /* Workspace bytes currently held by the handle: the sum over the plans of
- * every signature seen (the plans' small device tables not included). */
+ * every signature seen (the plans' small device tables not included), and the
+ * blocks of the layer operators. */
 int64_t muon_workspace_bytes(const muon_handle *h);
 
 /* Free the handle and its workspace (waits for the device).  NULL is a no-op. */

@@ -63,7 +63,11 @@ struct DeviceGuard {
 // The handle's workspaces for these operators.  A block that has been handed
 // out may be read by a captured graph, so no block is freed before the handle:
 // a call takes the smallest one that is large enough, and only when there is
-// none is a new one allocated, of at least twice the largest.
+// none is a new one allocated, of twice the largest or more.  So the blocks of
+// calls that grow a little at a time are few, and all of them together hold
+// less than four times what the largest call needs (the last block less than
+// twice that, the ones before it less than the last).  Where twice the largest
+// cannot be had, the new block is what the call needs.
 struct LayerState : HandleExt {
     struct Block {
         void* p;
@@ -110,18 +114,22 @@ muon_status workspace(HandleBase* h, size_t bytes, hipStream_t stream, void** ou
                     "(its workspace is then resident)");
     if (h->flags & MUON_INIT_FAIL_ALLOC)
         return fail(h, MUON_ERR_OOM, "workspace allocation failed (forced by MUON_INIT_FAIL_ALLOC)");
-    // doubled where that is small, so that growing sizes leave few blocks behind
-    size_t want = std::max(bytes, std::min(2 * largest, size_t(1) << 28));
-    want = (want + 0xFFFFFu) & ~size_t(0xFFFFF);
-    LayerState::Block b{nullptr, want};
+    auto mib = [](size_t n) { return (n + 0xFFFFFu) & ~size_t(0xFFFFF); };
+    LayerState::Block b{nullptr, mib(std::max(bytes, 2 * largest))};
     try {
         st.blocks.reserve(st.blocks.size() + 1);
     } catch (const std::bad_alloc&) {
         return fail(h, MUON_ERR_OOM, "workspace allocation failed");
     }
-    if (hipMalloc(&b.p, want) != hipSuccess) {
+    bool got = hipMalloc(&b.p, b.bytes) == hipSuccess;
+    if (!got && b.bytes > mib(bytes)) {
         (void)hipGetLastError();
-        return fail(h, MUON_ERR_OOM, "workspace allocation of %.3f GB failed", double(want) / 1e9);
+        b.bytes = mib(bytes);
+        got = hipMalloc(&b.p, b.bytes) == hipSuccess;
+    }
+    if (!got) {
+        (void)hipGetLastError();
+        return fail(h, MUON_ERR_OOM, "workspace allocation of %.3f GB failed", double(b.bytes) / 1e9);
     }
     st.blocks.push_back(b);
     *out = b.p;

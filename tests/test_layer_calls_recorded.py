@@ -59,3 +59,53 @@ def test_empty_tensors_with_an_activation():
         torch.cuda.synchronize()
     finally:
         nsm.muon_destroy(h)
+
+
+MIB = 1 << 20
+
+
+def _needs(call, lines):
+    """What each call allocates on a handle of its own."""
+    cmds = []
+    for s in lines:
+        cmds += ["new", s]
+    return [r["workspace"] for r in call(*cmds)]
+
+
+# 8-bit layer inputs decoded in the workspace: 2 rows x in bytes, from small to past 256 MiB
+GROWING = [f"dw {r} 8192 8192 x8 db" for r in range(1000, 100001, 1000)]
+
+
+def test_growing_calls_hold_a_bounded_workspace(call):
+    """Batches that grow a little at a time: what the handle holds stays under
+    four times the largest need (plus the rounding of each block to a MiB), at
+    every call, and only a few blocks are ever allocated."""
+    need = _needs(call, GROWING)
+    held = [r["workspace"] for r in call(*GROWING)]
+    assert max(need) > 1024 * MIB and need == sorted(need)
+    for n, b in zip(need, held):
+        assert n <= b <= 4 * n + 32 * MIB
+    assert len(set(held)) <= 12
+    # smaller calls afterwards, in any order, allocate nothing
+    again = call(*GROWING, *reversed(GROWING))
+    assert again[-1]["workspace"] == held[-1]
+
+
+def test_growth_falls_back_to_the_size_needed(call):
+    """Where twice the largest block cannot be allocated, the call's own size is."""
+    lines = [f"dw {r} 8192 8192 x8" for r in (20000, 24000)]
+    n = _needs(call, lines)
+    a, b = call(lines[0], f"limit {n[1]}", lines[1])
+    assert a["status"] == OK and b["status"] == OK and a["workspace"] == n[0] and b["workspace"] == sum(n)
+    a, b = call(lines[0], f"limit {n[1] - MIB}", lines[1])
+    assert b["status"] == OOM and b["launches"] == [] and b["workspace"] == n[0]
+
+
+def test_capture_finds_a_block_or_is_refused(call):
+    big, small = "dw 20000 8192 8192 x8", "dw 10000 8192 8192 x8"
+    a, = call(small + " capture")
+    assert a["status"] == INVALID and a["launches"] == [] and a["workspace"] == 0
+    a, b, c = call(small, small + " capture", big + " capture")
+    assert (a["status"], b["status"], c["status"]) == (OK, OK, INVALID) and c["workspace"] == a["workspace"]
+    a, b = call(big, small + " capture")
+    assert b["status"] == OK and b["workspace"] == a["workspace"]
