@@ -400,27 +400,28 @@ muon_status muon_adamw_step(muon_handle *h, const muon_adamw_tensor *tensors, in
  *
  * Conventions of the seven layer operators: every matrix is row-major with a
  * leading dimension in elements; any alignment of the element type and any
- * size is taken (16-byte aligned rows of whole 16-byte chunks run fastest);
- * rows == 0 enqueues nothing (every matrix with a row per token may then be
- * NULL), except that the gradients of parameters are zeroed (or left, with
- * accumulate).  Nothing but the named outputs is
- * written: a leading dimension's padding keeps its values.  Outputs may not be
- * inputs or each other except where noted (base addresses are compared).
+ * size within the limits named is taken (16-byte aligned rows of whole 16-byte
+ * chunks run fastest); rows == 0 enqueues nothing (every matrix with a row per
+ * token may then be NULL), except that the gradients of parameters are zeroed
+ * (or left, with accumulate).  Nothing but the named outputs is written: a
+ * leading dimension's padding keeps its values.  Outputs may not be inputs or
+ * each other except where noted (base addresses are compared).
  * Results do not depend on timing: the same call gives the same bits.  They
  * are not among the profiled roles.  Workspaces belong to the handle and grow
  * in blocks, each at least twice the one before (of the size needed where that
  * cannot be had), of which none is freed or moved until muon_destroy, as a
  * graph may use it: doubled blocks together hold less than four times what the
- * largest call needs.  Calls on one handle share them and
- * must be ordered, like those of muon_step (graphs captured from one handle
- * too, when they are replayed).  A call captured into a HIP graph must find its
- * workspace large enough, so a call of the same sizes, leading dimensions and
- * alignments must have run once outside capture (MUON_ERR_INVALID_ARG
- * otherwise).  Errors: MUON_ERR_INVALID_ARG (a null handle, argument struct
- * or required pointer, a size or leading dimension out of range, aliasing, an
- * unknown activation or weight layout, both z and z8, act_out without either, an
- * activation without either in muon_linear_grad_input, flags other than 0 and
- * 1, reserved != 0), MUON_ERR_DTYPE, MUON_ERR_OOM, MUON_ERR_HIP. */
+ * largest call needs.  Calls on one handle share them and must be ordered, like
+ * those of muon_step (graphs captured from one handle too, when they are
+ * replayed).  A call captured into a HIP graph must find its workspace large
+ * enough, so a call of the same sizes, leading dimensions and alignments must
+ * have run once outside capture (MUON_ERR_INVALID_ARG otherwise).  Errors: MUON_ERR_INVALID_ARG (a null handle, argument struct
+ * or required pointer, a size or leading dimension out of range, a product of
+ * more than 2^24 - 8 output tiles of 128 x 128, 2^23 rows or more of a norm
+ * past 16384 columns, aliasing, an unknown activation or weight layout, both z
+ * and z8, act_out without either, an activation without either in
+ * muon_linear_grad_input, flags other than 0 and 1, reserved != 0),
+ * MUON_ERR_DTYPE, MUON_ERR_OOM, MUON_ERR_HIP. */
 muon_status muon_layernorm_forward(muon_handle *h, const muon_layernorm_args *args, void *stream);
 
 /* Its gradient: with xh = (x - mean) rstd and a = dy gain,

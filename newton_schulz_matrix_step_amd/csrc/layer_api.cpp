@@ -27,7 +27,6 @@ namespace {
 constexpr int64_t kMaxCols = int64_t(1) << 20;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxLd = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 
 muon_status fail(HandleBase* h, muon_status st, const char* fmt, ...) {
     char buf[512];
@@ -222,7 +221,8 @@ bool operand_dma(const void* p, int64_t ld, int64_t contiguous, bool kc, int es)
 
 muon_status run_linear(HandleBase* h, LinArgs& a, hipStream_t stream) {
     const int64_t tiles = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-    if (tiles > kMaxGrid / 128) return fail(h, MUON_ERR_INVALID_ARG, "more than %lld output tiles", (long long)(kMaxGrid / 128));
+    if (tiles > kMaxTiles128)
+        return fail(h, MUON_ERR_INVALID_ARG, "more than %lld output tiles of 128 x 128", (long long)kMaxTiles128);
     DeviceGuard g(h->device);
     if (!g.ok) return fail(h, MUON_ERR_NO_DEVICE, "cannot select device %d", h->device);
     const LinPlan p = plan_linear(a);
@@ -258,6 +258,7 @@ muon_status layernorm_forward(muon_handle* handle, const muon_layernorm_args* ar
     ck.dtype(p.param_dtype, "gain");
     ck.size(p.rows, 0, kMaxRows, "rows");
     ck.size(p.cols, 1, kMaxCols, "cols");
+    ck.need(norm_rows_fit(p.rows, p.cols), "too many rows of %lld columns", (long long)p.cols);
     ck.need(p.reserved == 0, "reserved field must be 0");
     ck.need(std::isfinite(p.eps) && p.eps >= 0.f, "eps must be finite and >= 0");
     ck.need(p.rows == 0 || (p.x && p.y), "x or y is NULL");
@@ -305,6 +306,7 @@ muon_status layernorm_backward(muon_handle* handle, const muon_layernorm_grad_ar
     ck.dtype(p.param_dtype, "gain");
     ck.size(p.rows, 0, kMaxRows, "rows");
     ck.size(p.cols, 1, kMaxCols, "cols");
+    ck.need(norm_rows_fit(p.rows, p.cols), "too many rows of %lld columns", (long long)p.cols);
     ck.need(p.reserved == 0, "reserved field must be 0");
     ck.need(p.accumulate == 0 || p.accumulate == 1, "accumulate must be 0 or 1, got %d", p.accumulate);
     ck.need(p.rows == 0 || (p.dy && p.x && p.mean && p.rstd && p.dx), "dy, x, mean, rstd or dx is NULL");

@@ -31,6 +31,17 @@ HandleBase* handle_base(muon_handle* h);   // muon_api.cpp
 
 constexpr int kAct8Group = 32;             // columns that share one exponent
 
+// A launch has fewer than 2^32 threads along a dimension of its grid.  Passes
+// over the rows of one matrix go in slices of at most 2^31 (MUON_SLICE_THREADS:
+// smaller in a build that checks them); a product or a norm of long rows that
+// would need more is refused.
+#ifndef MUON_SLICE_THREADS
+#define MUON_SLICE_THREADS (int64_t(1) << 31)
+#endif
+constexpr int64_t kGridThreads = int64_t(1) << 32;
+constexpr int64_t kSliceThreads = MUON_SLICE_THREADS;
+constexpr int64_t kMaxTiles128 = kGridThreads / 256 - 8;   // 128-wide output tiles, of 256 threads, in eighths
+
 // 8-bit checkpoint as the kernels take it: element (r, c) is
 // codes[r * ld + c] * 2^(exps[r * lde + c / 32] - 127).
 struct Act8View {
@@ -75,6 +86,8 @@ struct NormGradArgs {
 
 // Workgroups (= rows of the partial sums) of the backward pass.
 int norm_grad_parts(int64_t rows, int cols);
+// Whether the norm's launches can take so many rows.
+bool norm_rows_fit(int64_t rows, int64_t cols);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s);
 

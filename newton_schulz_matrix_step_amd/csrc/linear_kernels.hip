@@ -1150,17 +1150,22 @@ __global__ __launch_bounds__(256) void linear_pack_kernel(const T* src, int64_t 
         }
     *reinterpret_cast<GMEM u32x4_t*>(gm(dst) + r * ldd + c) = u32x4_t{w[0], w[1], w[2], w[3]};
 }
+template <class T>
+hipError_t launch_pack_typed(const T* src, int64_t ld, T* dst, int64_t ldd, int64_t rows, int64_t cols, hipStream_t s) {
+    const int64_t cpr = ldd / Num<T>::EPC, slice = (kSliceThreads + cpr - 1) / cpr;   // rows of a launch
+    for (int64_t r0 = 0; r0 < rows; r0 += slice) {
+        const int64_t nr = rows - r0 < slice ? rows - r0 : slice;
+        hipLaunchKernelGGL((linear_pack_kernel<T>), dim3(unsigned((nr * cpr + 255) / 256)), dim3(256), 0, s, src + r0 * ld,
+                           ld, dst + r0 * ldd, ldd, nr, cols);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
 hipError_t launch_pack(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int64_t cols, int dt,
                        hipStream_t s) {
-    const int64_t n = rows * (ldd / (dt == 0 ? 8 : 4));
-    const dim3 grid(unsigned((n + 255) / 256)), block(256);
-    if (dt == 0)
-        hipLaunchKernelGGL((linear_pack_kernel<uint16_t>), grid, block, 0, s, static_cast<const uint16_t*>(src), ld,
-                           static_cast<uint16_t*>(dst), ldd, rows, cols);
-    else
-        hipLaunchKernelGGL((linear_pack_kernel<float>), grid, block, 0, s, static_cast<const float*>(src), ld,
-                           static_cast<float*>(dst), ldd, rows, cols);
-    return hipGetLastError();
+    return dt == 0 ? launch_pack_typed(static_cast<const uint16_t*>(src), ld, static_cast<uint16_t*>(dst), ldd, rows, cols, s)
+                   : launch_pack_typed(static_cast<const float*>(src), ld, static_cast<float*>(dst), ldd, rows, cols, s);
 }
 
 template <class T, bool AKC, bool BKC, int ASRC, int BSRC, int KIND, bool TR>
@@ -1289,6 +1294,7 @@ LinPlan plan_linear(const LinArgs& a) {
             for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
                 const int64_t per = (nkb + s - 1) / s;
                 if (s > 1 && (nkb + per - 1) / per != s) continue;   // it would leave a split empty
+                if ((tiles * s + 7) / 8 * 8 * (tc.edge == 256 ? 512 : 256) >= kGridThreads) continue;
                 const double w = double(tiles * s) / 256;            // workgroups a CU
                 double us;
                 if (tc.edge == 256) us = 3 + std::ceil(w) * (tc.fixed + block * double(per));

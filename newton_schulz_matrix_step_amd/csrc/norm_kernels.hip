@@ -556,6 +556,10 @@ int norm_grad_parts(int64_t rows, int cols) {
     return int(n < kMaxGradParts ? n : kMaxGradParts);
 }
 
+// The looping kernels of rows past 16384 columns take one workgroup a row (so
+// many would be more than 275 GB).
+bool norm_rows_fit(int64_t rows, int64_t cols) { return cols <= 16384 || rows * kNT < kGridThreads; }
+
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;
     const bool reg = pick_row(a.cols, [&](auto nw, auto e) {
@@ -603,29 +607,30 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
 }
 
 namespace {
-void act8_geometry(const Act8Args& a, int& rpb, int& slots, unsigned& grid) {
-    slots = (a.cols + kAct8Group - 1) / kAct8Group * (kAct8Group / 8);
-    rpb = slots >= 1024 ? 1 : 1024 / slots;
-    grid = unsigned((a.rows + rpb - 1) / rpb);
+
+// One launch, or more past 2^31 threads, each of whole workgroups' rows.
+template <class K>
+hipError_t launch_act8(const Act8Args& a, K* kernel, hipStream_t s) {
+    const int slots = (a.cols + kAct8Group - 1) / kAct8Group * (kAct8Group / 8);
+    const int rpb = slots >= 1024 ? 1 : 1024 / slots;
+    const int64_t slice = (kSliceThreads + 255) / 256 * rpb, es = a.dt == 0 ? 2 : 4;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += slice) {
+        Act8Args b = a;
+        b.rows = a.rows - r0 < slice ? a.rows - r0 : slice;
+        if (a.x) b.x = static_cast<const char*>(a.x) + r0 * a.ld * es;
+        if (a.y) b.y = static_cast<char*>(a.y) + r0 * a.ld * es;
+        b.q.codes += r0 * a.q.ld;
+        b.q.exps += r0 * a.q.lde;
+        hipLaunchKernelGGL(kernel, dim3(unsigned((b.rows + rpb - 1) / rpb)), dim3(256), 0, s, b, rpb, slots);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
+
 }  // namespace
 
-hipError_t launch_act8_encode(const Act8Args& a, hipStream_t s) {
-    if (a.rows <= 0) return hipSuccess;
-    int rpb, slots;
-    unsigned grid;
-    act8_geometry(a, rpb, slots, grid);
-    hipLaunchKernelGGL(act8_encode_kernel, dim3(grid), dim3(256), 0, s, a, rpb, slots);
-    return hipGetLastError();
-}
-
-hipError_t launch_act8_decode(const Act8Args& a, hipStream_t s) {
-    if (a.rows <= 0) return hipSuccess;
-    int rpb, slots;
-    unsigned grid;
-    act8_geometry(a, rpb, slots, grid);
-    hipLaunchKernelGGL(act8_decode_kernel, dim3(grid), dim3(256), 0, s, a, rpb, slots);
-    return hipGetLastError();
-}
+hipError_t launch_act8_encode(const Act8Args& a, hipStream_t s) { return launch_act8(a, act8_encode_kernel, s); }
+hipError_t launch_act8_decode(const Act8Args& a, hipStream_t s) { return launch_act8(a, act8_decode_kernel, s); }
 
 }  // namespace muon

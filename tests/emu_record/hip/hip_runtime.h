@@ -52,7 +52,7 @@ inline hipError_t emu_limited_malloc(T** p, size_t n) {
         *p = nullptr;
         return 2;
     }
-    return hipMalloc(p, n);
+    return hipMalloc(p, n < 64 ? n : 64);   // only its address is used
 }
 #define hipMalloc emu_limited_malloc
 inline hipError_t emu_capturing(hipStream_t s, hipStreamCaptureStatus* st) {

@@ -109,3 +109,35 @@ def test_capture_finds_a_block_or_is_refused(call):
     assert (a["status"], b["status"], c["status"]) == (OK, OK, INVALID) and c["workspace"] == a["workspace"]
     a, b = call(big, small + " capture")
     assert b["status"] == OK and b["workspace"] == a["workspace"]
+
+
+# Calls whose natural grid has 2^32 threads or more, which no launch can have:
+# many rows of a narrow product, 8-bit checkpoints and operands of tens of GB.
+WIDE_GRIDS = ["fwd 2147482000 8 8", "fwd 1073741824 8 8 oi", "fwd 2147482624 16 8 f32", "dx 2147482000 8 8",
+              "dx 1073741825 16 24 f32 z8 act=1 actout", "fwd 8 8 1048576 bias", "dw 64 1048576 262016", "fwd 2147482000 37 40", "dw 2147483647 7 9 db f32",
+              "enc 16777216 4104 0", "enc 33554432 4104 0", "enc 16777217 8192 0 f32", "dec 33554432 4104 0",
+              "enc 2147483647 32 0", "dec 2147483647 1 0", "ln 2147483647 8 0 y8", "lngrad 2147483647 64 0 add"]
+
+
+@pytest.mark.parametrize("line", WIDE_GRIDS)
+def test_launches_stay_under_2_32_threads(call, line):
+    r, = call(line)
+    assert r["status"] == OK and r["launches"], r
+    for k in r["launches"]:
+        assert 0 < k["grid"] * k["block"] < 2 ** 32, k
+
+
+@pytest.mark.parametrize("line", ["fwd 2147483647 8 8", "fwd 2147482625 8 8", "dx 1073741825 1048576 8", "dw 8 1048576 1048576",
+                                  "ln 8388608 16392 0", "lngrad 8388608 16392 0"])
+def test_more_than_a_launch_can_take_is_refused(call, line):
+    r, = call(line)
+    assert r["status"] == INVALID and r["launches"] == [], r
+
+
+def test_checkpoint_slices_cover_every_row(call):
+    """A checkpoint pass in several launches: workgroups of one row each, as many as rows."""
+    for op in ("enc", "dec"):
+        r, = call(f"{op} 33554433 4104 0")
+        assert len(r["launches"]) > 1 and sum(k["grid"] for k in r["launches"]) == 33554433
+        r, = call(f"{op} 16384 4096 0")
+        assert [k["grid"] for k in r["launches"]] == [8192]
