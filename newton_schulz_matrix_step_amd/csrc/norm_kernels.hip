@@ -53,11 +53,8 @@ struct RowRaw {
 
 // A row exactly as loaded (decoded where it is used, so that the wait for the
 // load falls there); columns past the end read as zeros.  STREAM: the row is not
-// kept in the caches.  The forward streams its output, which then need not be
-// written back from the L2s at the kernel's end (8191 x 2048 float32 28.4 ->
-// 22.9 us; loads streamed as well 24.0, loads alone 26.2).  The backward streams
-// what it reads (8192 x 4096 bf16 with an added gradient 64.4 -> 61.4 us; stores
-// 63.6, both 63.8).
+// kept in the caches.  The backward streams what it reads (8192 x 4096 bf16 with
+// an added gradient 64.4 -> 61.4 us; stores 63.6, both 63.8).
 template <class T, bool VEC, int NW, int E, bool STREAM = false>
 __device__ __forceinline__ void row_load(const void* p, int64_t base, int cols, int lane, bool on,
                                          RowRaw<T, VEC, NW, E>& r) {
@@ -209,7 +206,7 @@ __device__ __forceinline__ void row_store_act8(const Act8View& q, int64_t row, i
     }
 }
 
-template <class T, bool VEC, int NW, int E>
+template <class T, bool VEC, int NW, int E, bool STREAM>
 __global__ __launch_bounds__(kNT) void norm_kernel(NormArgs a) {
     using G = RowGeom<T, VEC, NW, E>;
     constexpr int RB = kWaves / NW;      // rows a workgroup works on at once
@@ -254,7 +251,7 @@ __global__ __launch_bounds__(kNT) void norm_kernel(NormArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < E; ++i) v[i] = a.bias ? fmaf(v[i] * r, g[i], b[i]) : v[i] * r * g[i];
-        if (on) row_store<T, VEC, NW, E, true>(a.y, row * a.ld_y, a.cols, lane, v);
+        if (on) row_store<T, VEC, NW, E, STREAM>(a.y, row * a.ld_y, a.cols, lane, v);
         if (a.y8.codes) row_store_act8<T, VEC, NW, E>(a.y8, row, a.cols, lane, on, v);
     }
 }
@@ -562,18 +559,27 @@ bool norm_rows_fit(int64_t rows, int64_t cols) { return cols <= 16384 || rows * 
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;
+    // y is stored past the caches where the L2s (32 MiB) cannot hold it for its
+    // reader anyway; it need then not be written back at the kernel's end: 8191 x
+    // 2048 float32 27.2 -> 25.1 us, 8192 x 4096 bf16 26.5 -> 25.6, and with the
+    // product that reads it (4096 -> 4096) 227 both ways.  Under that the product
+    // finds y in the caches, which is worth more than the norm itself gains: 2048 x
+    // 768 with 768 -> 768 13.6 us kept and 14.3 streamed (the norm alone 4.9, 4.8),
+    // 4096 x 1024 with 1024 -> 4096 40.7 and 41.3 (6.7, 6.0).
+    const bool stream = a.rows * a.cols * (a.dt == 0 ? 2 : 4) > (32ll << 20);
     const bool reg = pick_row(a.cols, [&](auto nw, auto e) {
         constexpr int NW = decltype(nw)::value, E = decltype(e)::value;
         constexpr int RB = kWaves / NW;
         const int64_t nb = (a.rows + RB - 1) / RB;
         const dim3 grid(unsigned(nb < kMaxFwdBlocks ? nb : kMaxFwdBlocks)), block(kNT);
-        if (a.dt == 0) {
-            if (a.vec) hipLaunchKernelGGL((norm_kernel<uint16_t, true, NW, E>), grid, block, 0, s, a);
-            else hipLaunchKernelGGL((norm_kernel<uint16_t, false, NW, E>), grid, block, 0, s, a);
-        } else {
-            if (a.vec) hipLaunchKernelGGL((norm_kernel<float, true, NW, E>), grid, block, 0, s, a);
-            else hipLaunchKernelGGL((norm_kernel<float, false, NW, E>), grid, block, 0, s, a);
-        }
+        auto go = [&](auto zero) {
+            using T = decltype(zero);
+            if (!a.vec) hipLaunchKernelGGL((norm_kernel<T, false, NW, E, false>), grid, block, 0, s, a);
+            else if (stream) hipLaunchKernelGGL((norm_kernel<T, true, NW, E, true>), grid, block, 0, s, a);
+            else hipLaunchKernelGGL((norm_kernel<T, true, NW, E, false>), grid, block, 0, s, a);
+        };
+        if (a.dt == 0) go(uint16_t{});
+        else go(float{});
     });
     if (!reg) hipLaunchKernelGGL(norm_long_kernel, dim3(unsigned(a.rows)), dim3(kNT), 0, s, a);
     return hipGetLastError();

@@ -219,9 +219,12 @@ def test_product_kernel(nsm, h, line):
 
 # Rows of 2, 4 and 8 waves (and one of 32 elements a lane), in vectors and not,
 # enough of them that each workgroup takes at least three rows forward and six
-# backward, the last turn ragged: 512 workgroups of 4, 2 or 1 rows forward, 256 backward.
+# backward, the last turn ragged: 512 workgroups of 4, 2 or 1 rows forward, 256
+# backward.  Then outputs over and under the size from which they are streamed,
+# for each number of waves and both types.
 NORM_SHAPES = [(7001, 2048), (7001, 1030), (3501, 4096), (3501, 4095), (1801, 8192), (1801, 8191), (1801, 12288),
-               (1801, 9001)]
+               (1801, 9001), (18001, 1000), (9001, 2048), (4500, 4096), (2200, 8192), (5000, 776), (3001, 2048),
+               (1201, 4096), (700, 8192), (300, 12288)]
 
 
 def depth(cols):

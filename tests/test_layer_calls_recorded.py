@@ -141,3 +141,17 @@ def test_checkpoint_slices_cover_every_row(call):
         assert len(r["launches"]) > 1 and sum(k["grid"] for k in r["launches"]) == 33554433
         r, = call(f"{op} 16384 4096 0")
         assert [k["grid"] for k in r["launches"]] == [8192]
+
+
+@pytest.mark.parametrize("line,streams", [("ln 16 768 0", False), ("ln 2048 768 0 bias y8", False), ("ln 8192 2048 0", False),
+                                          ("ln 8193 2048 0", True), ("ln 8192 4096 0 bias", True), ("ln 4096 2048 0 f32", False),
+                                          ("ln 8191 2048 0 f32 y8", True), ("ln 5000 12288 0", True), ("ln 9001 4095 0", None),
+                                          ("ln 70000 1024 0 shift=1", None)])
+def test_only_outputs_past_the_caches_are_streamed(call, line, streams):
+    """A norm's output is what the next product reads: it is stored past the L2s
+    only where they could not hold it (None: rows without whole 16-byte runs, by element)."""
+    r, = call(line)
+    k, = r["launches"]
+    words = k["kernel"].strip("()").replace(">", "").split(", ")
+    assert words[-1] == ("true" if streams else "false"), k
+    assert words[1] == ("false" if streams is None else "true"), k
