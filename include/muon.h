@@ -177,10 +177,11 @@ typedef struct muon_adamw_hparams {
  *
  * The encoder takes the smallest power of two, not under 2^-126, that keeps
  * every code of the group within -127..127, and rounds to nearest even: an
- * element is off by at most half a step, 2^-7 of its group's largest magnitude
- * (2^-8 at best).  Decoding is exact in bfloat16 and float32.  A group holding
- * an infinity or a NaN gets exponent byte 255 and codes 0: all of it decodes to
- * NaN.  The encoder writes bytes 1..249 and 255; byte 0 decodes to zeros. */
+ * element is off by at most half a step, 1/127 of its group's largest magnitude
+ * (1/254 at best), or, in a group under 63.5 * 2^-126, 2^-127.  Decoding is
+ * exact in bfloat16 and float32.  A group holding an infinity or a NaN gets
+ * exponent byte 255 and codes 0: all of it decodes to NaN.  The encoder writes
+ * bytes 1..249 and 255; byte 0 decodes to zeros. */
 typedef struct muon_act8 {
     int8_t  *codes;            /* rows x cols */
     uint8_t *exponents;        /* rows x ceil(cols / 32) */
