@@ -396,8 +396,9 @@ muon_status muon_adamw_step(muon_handle *h, const muon_adamw_tensor *tensors, in
  *   mean = sum x / cols;  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
  *   y = (x - mean) rstd gain + bias
  *
- * in float32, y rounded once to its dtype.  mean and rstd are kept for the
- * backward pass, y8 holds y for the weight gradient of the layer it feeds.
+ * in float32 (squares past its range make the variance infinite), y rounded
+ * once to its dtype.  mean and rstd are kept for the backward pass, y8 holds y
+ * for the weight gradient of the layer it feeds.
  *
  * Conventions of the seven layer operators: every matrix is row-major with a
  * leading dimension in elements; any alignment of the element type and any
@@ -422,7 +423,8 @@ muon_status muon_adamw_step(muon_handle *h, const muon_adamw_tensor *tensors, in
  * past 16384 columns, aliasing, an unknown activation or weight layout, both z
  * and z8, act_out without either, an activation without either in
  * muon_linear_grad_input, flags other than 0 and 1, reserved != 0),
- * MUON_ERR_DTYPE, MUON_ERR_OOM, MUON_ERR_HIP. */
+ * MUON_ERR_DTYPE, MUON_ERR_NO_DEVICE (the handle's device cannot be selected),
+ * MUON_ERR_OOM, MUON_ERR_HIP. */
 muon_status muon_layernorm_forward(muon_handle *h, const muon_layernorm_args *args, void *stream);
 
 /* Its gradient: with xh = (x - mean) rstd and a = dy gain,

@@ -820,10 +820,11 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a) {
 // but the 6 halves issued last (2 loads a wave each) has landed.  Loads past the
 // end of k are issued too and read as zeros, which keeps that count.
 //
-// MFMA bound (its pipes are busy about 70 % of the time, no LDS bank conflict):
-// 4096 tokens 14336 -> 4096 with a residual 333 us, 1.44 PFLOP/s; short k is
+// Long k is MFMA bound (pipes busy about 70 % of the time, no LDS bank conflict):
+// 4096 tokens 14336 -> 4096 with a residual 335 us, 1.44 PFLOP/s.  Short k is
 // carried by prologue and epilogue: 8192 tokens 1024 -> 4096 with bias and GELU
-// 78.5 us, 0.88 PFLOP/s (one workgroup a CU: nothing overlaps its epilogue).
+// 75-80 us, 0.86-0.91 PFLOP/s, pipes busy 41 % (one workgroup a CU: nothing
+// overlaps its epilogue).
 // ---------------------------------------------------------------------------
 constexpr int kPpThreads = 512;
 

@@ -9,6 +9,10 @@
 // All of them stream rows once: HBM bound.  A row lies in the registers of NW
 // waves (E elements a lane, in 16-byte runs), so both passes over it (mean,
 // then centred squares; the two row sums, then dx) read it from memory once.
+// That holds to 8192 columns.  With 32 elements a lane (to 16384) the backward
+// kernel spills 283-566 VGPRs to scratch, the forward one without 16-byte
+// vectors 80: 4096 x 12288 bf16 backward with an added gradient 182 us where its
+// bytes take 78, 4096 x 8192 67 where they take 52.
 // Statistics and sums are float32.
 
 #include <type_traits>
@@ -469,8 +473,8 @@ __global__ __launch_bounds__(kNT) void norm_grad_join_kernel(NormGradArgs a) {
 
 // ---- 8-bit checkpoints: 8 elements a lane, 4 lanes a group ----
 // A workgroup takes RPB rows of `slots` 8-element runs each (padded to whole
-// groups).  HBM bound: 16384 x 4096 bf16 encoded and decoded in 79-80 us, 406 MB
-// at 5.1 TB/s.
+// groups).  HBM bound: 16384 x 4096 bf16 encoded and decoded in 81 us, 406 MB at
+// 5.0 TB/s.
 __global__ __launch_bounds__(256) void act8_encode_kernel(Act8Args a, int rpb, int slots) {
     const int64_t r0 = int64_t(blockIdx.x) * rpb;
     const int n = rpb * slots;           // multiple of 4; every lane of a group runs the same steps
@@ -539,7 +543,7 @@ bool pick_row(int cols, F&& f) {
 }
 int row_waves(int cols) { return cols <= 1024 ? 1 : cols <= 2048 ? 2 : cols <= 4096 ? 4 : 8; }
 
-// Forward: two workgroups a CU (8192 x 4096 bf16 27.5 us; four a CU 29.4).
+// Forward: two workgroups a CU (8192 x 4096 bf16 27.5 us, kept stores; four a CU 29.4).
 // Backward: one (45.8 us; half as many 64.5, half as many again 58).
 constexpr int kMaxFwdBlocks = 512;
 constexpr int kMaxGradParts = 256;
