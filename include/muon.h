@@ -410,21 +410,21 @@ muon_status muon_adamw_step(muon_handle *h, const muon_adamw_tensor *tensors, in
  * each other except where noted (base addresses are compared).
  * Results do not depend on timing: the same call gives the same bits.  They
  * are not among the profiled roles.  Workspaces belong to the handle and grow
- * in blocks, each at least twice the one before (of the size needed where that
- * cannot be had), of which none is freed or moved until muon_destroy, as a
- * graph may use it: doubled blocks together hold less than four times what the
- * largest call needs.  Calls on one handle share them and must be ordered, like
- * those of muon_step (graphs captured from one handle too, when they are
+ * in blocks of whole MiB, each at least twice the one before (of the size needed
+ * where that cannot be had), of which none is freed or moved until muon_destroy,
+ * as a graph may use it: doubled blocks together hold less than four times what
+ * the largest call needs.  Calls on one handle share them and must be ordered,
+ * like those of muon_step (graphs captured from one handle too, when they are
  * replayed).  A call captured into a HIP graph must find its workspace large
  * enough, so a call of the same sizes, leading dimensions and alignments must
- * have run once outside capture (MUON_ERR_INVALID_ARG otherwise).  Errors: MUON_ERR_INVALID_ARG (a null handle, argument struct
- * or required pointer, a size or leading dimension out of range, a product of
- * more than 2^24 - 8 output tiles of 128 x 128, 2^23 rows or more of a norm
- * past 16384 columns, aliasing, an unknown activation or weight layout, both z
- * and z8, act_out without either, an activation without either in
- * muon_linear_grad_input, flags other than 0 and 1, reserved != 0),
- * MUON_ERR_DTYPE, MUON_ERR_NO_DEVICE (the handle's device cannot be selected),
- * MUON_ERR_OOM, MUON_ERR_HIP. */
+ * have run once outside capture (MUON_ERR_INVALID_ARG otherwise).  Errors:
+ * MUON_ERR_INVALID_ARG (a null handle, argument struct or required pointer, a
+ * size or leading dimension out of range, a product of more than 2^24 - 8 output
+ * tiles of 128 x 128, 2^23 rows or more of a norm past 16384 columns, aliasing,
+ * an unknown activation or weight layout, both z and z8, act_out without either,
+ * an activation without either in muon_linear_grad_input, flags other than 0 and
+ * 1, reserved != 0), MUON_ERR_DTYPE, MUON_ERR_NO_DEVICE (the handle's device
+ * cannot be selected), MUON_ERR_OOM, MUON_ERR_HIP. */
 muon_status muon_layernorm_forward(muon_handle *h, const muon_layernorm_args *args, void *stream);
 
 /* Its gradient: with xh = (x - mean) rstd and a = dy gain,
