@@ -559,7 +559,7 @@ int norm_grad_parts(int64_t rows, int cols) {
 
 // The looping kernels of rows past 16384 columns take one workgroup a row (so
 // many would be more than 275 GB).
-bool norm_rows_fit(int64_t rows, int64_t cols) { return cols <= 16384 || rows * kNT < kGridThreads; }
+bool norm_rows_fit(int64_t rows, int64_t cols) { return cols <= 16384 || rows < kGridThreads / kNT; }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;

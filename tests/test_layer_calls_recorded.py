@@ -128,7 +128,8 @@ def test_launches_stay_under_2_32_threads(call, line):
 
 
 @pytest.mark.parametrize("line", ["fwd 2147483647 8 8", "fwd 2147482625 8 8", "dx 1073741825 1048576 8", "dw 8 1048576 1048576",
-                                  "ln 8388608 16392 0", "lngrad 8388608 16392 0"])
+                                  "ln 8388608 16392 0", "lngrad 8388608 16392 0", "ln 9223372036854775807 20000 0",
+                                  "enc 9223372036854775807 20000 0", "fwd 9223372036854775807 8 8"])
 def test_more_than_a_launch_can_take_is_refused(call, line):
     r, = call(line)
     assert r["status"] == INVALID and r["launches"] == [], r
