@@ -1,7 +1,8 @@
 /*
  * muon.h -- C ABI of the MI355X (gfx950) Muon optimizer step, and of the layer
  * operators that make the gradients it takes (layer norm, the linear layer's
- * products, 8-bit activation checkpoints; see "the layer operators" below).
+ * products, 8-bit activation checkpoints; see "the layer operators" below; the
+ * gated feed-forward, norms around a block and dropout; see "the block operators").
  *
  * One muon_step call performs, for every 2-D weight in a list, the Muon step the speedrun
  * pages describe:
@@ -47,7 +48,7 @@
 extern "C" {
 #endif
 
-#define MUON_ABI_VERSION 7
+#define MUON_ABI_VERSION 8
 
 typedef enum muon_status {
     MUON_OK = 0,
@@ -286,6 +287,159 @@ typedef struct muon_linear_grad_weight_args {
     int32_t     reserved;      /* must be 0 */
 } muon_linear_grad_weight_args;
 
+/* ---- the block operators: a gated feed-forward block and what stands around it ---- */
+
+/* The gate's activation, act(z); at infinite z the limits, forward and backward. */
+typedef enum muon_gate {
+    MUON_GATE_SILU = 0,        /* z / (1 + exp(-z)) */
+    MUON_GATE_GELU = 1,        /* as MUON_ACT_GELU */
+    MUON_GATE_SIGMOID = 2,     /* 1 / (1 + exp(-z)) */
+    MUON_GATE_RELU = 3         /* max(z, 0) */
+} muon_gate;
+
+/* Arguments of muon_gated_forward.  The two tensors of a pair have one leading
+ * dimension; a weight that holds both projections is two such views of it. */
+typedef struct muon_gated_args {
+    const void *x;             /* rows x in, `dtype` */
+    const void *w_gate, *w_up; /* in x hidden or hidden x in (w_layout), `dtype` */
+    const void *bias_gate, *bias_up;   /* hidden, `bias_dtype`; each optional */
+    void       *h;             /* rows x hidden, `dtype` */
+    void       *gate, *up;     /* rows x hidden, `dtype`: receive both pre-activations; both or neither */
+    muon_act8   gate8, up8;    /* or their 8-bit checkpoints, taken before any rounding */
+    int64_t     rows, in, hidden;      /* rows >= 0; 1 <= in, hidden <= 2^20 */
+    int64_t     ld_x, ld_w, ld_h, ld_z;    /* ld_z: of gate and up */
+    int32_t     dtype, bias_dtype;     /* muon_dtype */
+    int32_t     activation;    /* muon_gate */
+    int32_t     w_layout;      /* muon_weight_layout */
+    int32_t     reserved;      /* must be 0 */
+} muon_gated_args;
+
+/* Arguments of muon_gated_grad_hidden. */
+typedef struct muon_gated_grad_hidden_args {
+    const void *dy;            /* rows x out, `dtype`: the gradient behind the down projection */
+    const void *w_down;        /* hidden x out or out x hidden (w_layout), `dtype` */
+    const void *gate, *up;     /* rows x hidden, `dtype`: both pre-activations, or NULL and */
+    muon_act8   gate8, up8;    /* their 8-bit checkpoints (read) */
+    void       *dgate, *dup;   /* rows x hidden, `dtype` */
+    void       *h;             /* rows x hidden, `dtype`: receives act(gate) up; optional */
+    int64_t     rows, hidden, out;
+    int64_t     ld_dy, ld_w, ld_z, ld_dz, ld_h;    /* ld_z: of gate and up; ld_dz: of dgate and dup */
+    int32_t     dtype;
+    int32_t     activation;    /* muon_gate */
+    int32_t     w_layout;
+    int32_t     reserved;      /* must be 0 */
+} muon_gated_grad_hidden_args;
+
+/* Arguments of muon_gated_grad_input. */
+typedef struct muon_gated_grad_input_args {
+    const void *dgate, *dup;   /* rows x hidden, `dtype` */
+    const void *w_gate, *w_up; /* as in the forward pass */
+    const void *add;           /* rows x in, `dtype`, added last; optional; may be dx itself */
+    void       *dx;            /* rows x in, `dtype` */
+    int64_t     rows, in, hidden;
+    int64_t     ld_dz, ld_w, ld_add, ld_dx;
+    int32_t     dtype;
+    int32_t     w_layout;
+    int32_t     reserved;      /* must be 0 */
+} muon_gated_grad_input_args;
+
+/* Arguments of muon_gated_grad_weight. */
+typedef struct muon_gated_grad_weight_args {
+    const void *x;             /* rows x in, `dtype`; or NULL and */
+    muon_act8   x8;            /* its 8-bit checkpoint (read) */
+    const void *dgate, *dup;   /* rows x hidden, `dtype` */
+    void       *dw_gate, *dw_up;       /* in x hidden or hidden x in (w_layout), `dw_dtype` */
+    void       *db_gate, *db_up;       /* hidden, `db_dtype`; each optional */
+    int64_t     rows, in, hidden;
+    int64_t     ld_x, ld_dz, ld_dw;
+    int32_t     dtype, dw_dtype, db_dtype;
+    int32_t     w_layout;
+    int32_t     accumulate;    /* 1: the four outputs are added to */
+    int32_t     reserved;      /* must be 0 */
+} muon_gated_grad_weight_args;
+
+/* A dropout mask.  Nothing of it is stored: element (r, c) of a matrix takes 16
+ * bits of a counter-based generator, Philox 4x32 of ten rounds (Salmon, Moraes,
+ * Dror and Shaw 2011), with the key (seed mod 2^32, seed / 2^32) and the counter
+ * (c / 8, r, n mod 2^32, n / 2^32), n = offset (+ *step) mod 2^64: half c mod 2
+ * (0: the low one) of word (c / 2) mod 4.  With T = p * 65536 rounded to nearest
+ * (halves to even), an element whose bits are under T is dropped, and becomes 0
+ * whatever it was; the others are multiplied by 65536 / (65536 - T).  So a mask
+ * depends on the element's place in its matrix alone, and the same seed and
+ * offset give it again, forward and backward.  Give every use of a step its own
+ * offset, or its own seed. */
+typedef struct muon_dropout_mask {
+    float     p;               /* 0 <= p <= 1 */
+    int32_t   reserved;        /* must be 0 */
+    uint64_t  seed, offset;
+    const uint64_t *step;      /* optional device pointer (8-byte aligned), read when the kernel runs: a graph
+                                  whose caller counts it up draws a new mask with every replay */
+} muon_dropout_mask;
+
+/* Arguments of muon_dropout. */
+typedef struct muon_dropout_args {
+    const void *x;             /* rows x cols, `dtype` */
+    const void *add;           /* rows x cols, `dtype`, added after the mask; optional; may be y itself */
+    void       *y;             /* rows x cols, `dtype`; may be x itself (same leading dimension) */
+    muon_dropout_mask drop;
+    int64_t     rows, cols;    /* rows >= 0, 1 <= cols <= 2^20 */
+    int64_t     ld_x, ld_add, ld_y;
+    int32_t     dtype;
+    int32_t     reserved;      /* must be 0 */
+} muon_dropout_args;
+
+typedef enum muon_norm {
+    MUON_NORM_NONE = 0,
+    MUON_NORM_RMS = 1,         /* x / sqrt(sum x^2 / cols + eps) */
+    MUON_NORM_LAYER = 2        /* (x - mean) / sqrt(sum (x - mean)^2 / cols + eps) */
+} muon_norm;
+
+/* Arguments of muon_blocknorm_forward.  The residual stream (x, s) has
+ * `stream_dtype`, the block's own tensors (branch, y) `dtype`; the pair is
+ * bf16 and bf16, float32 and float32, or a float32 stream with bf16 blocks. */
+typedef struct muon_blocknorm_args {
+    const void *x;             /* rows x cols: the stream before the junction */
+    const void *branch;        /* rows x cols: the block's output; optional */
+    const void *post_gain, *post_bias; /* cols, `param_dtype`: of the branch's norm; optional (bias: layer norm only) */
+    const void *gate;          /* cols, `param_dtype`: factors of the branch's columns; optional */
+    const void *pre_gain, *pre_bias;   /* of the norm behind the junction; optional (bias: layer norm only) */
+    void       *s;             /* rows x cols: the stream behind the junction; may be x (same leading dimension);
+                                  NULL without a branch, where x is it */
+    void       *y;             /* rows x cols: its norm, the next block's input; NULL with pre_norm NONE */
+    muon_act8   y8;            /* y's 8-bit checkpoint, of y before its rounding; codes NULL = none */
+    float      *post_mean, *post_rstd, *pre_mean, *pre_rstd;   /* rows; each optional; means: layer norm only */
+    muon_dropout_mask drop;    /* of the branch, between its norm and its gate */
+    int64_t     rows, cols;    /* rows >= 0, 1 <= cols <= 2^20 */
+    int64_t     ld_x, ld_branch, ld_s, ld_y;
+    float       residual_scale, branch_scale;   /* finite */
+    float       post_eps, pre_eps;     /* >= 0, finite */
+    int32_t     post_norm, pre_norm;   /* muon_norm */
+    int32_t     stream_dtype, dtype, param_dtype;
+    int32_t     reserved;      /* must be 0 */
+} muon_blocknorm_args;
+
+/* Arguments of muon_blocknorm_backward. */
+typedef struct muon_blocknorm_grad_args {
+    const void *dy;            /* rows x cols, `dtype`: gradient at y; NULL with pre_norm NONE */
+    const void *ds;            /* rows x cols, `stream_dtype`: gradient at s from behind; optional beside dy */
+    const void *s;             /* rows x cols, `stream_dtype`: the stream behind the junction, as stored (x without a
+                                  branch); with pre_norm */
+    const void *branch;        /* rows x cols, `dtype`; with post_norm, or for dgate */
+    const void *post_gain, *post_bias, *gate, *pre_gain;
+    const float *post_mean, *post_rstd, *pre_mean, *pre_rstd;  /* as the forward pass wrote them */
+    void       *dx;            /* rows x cols, `stream_dtype`; may be ds itself (same leading dimension) */
+    void       *dbranch;       /* rows x cols, `dtype`; NULL: the junction had no branch */
+    void       *dpost_gain, *dpost_bias, *dgate, *dpre_gain, *dpre_bias;   /* cols, `param_dtype`; each optional */
+    muon_dropout_mask drop;
+    int64_t     rows, cols;
+    int64_t     ld_dy, ld_ds, ld_s, ld_branch, ld_dx, ld_dbranch;
+    float       residual_scale, branch_scale;
+    int32_t     post_norm, pre_norm;
+    int32_t     stream_dtype, dtype, param_dtype;
+    int32_t     accumulate;    /* 1: the parameters' gradients are added to */
+    int32_t     reserved;      /* must be 0 */
+} muon_blocknorm_grad_args;
+
 /* Version of this header the library was built from (MUON_ABI_VERSION). */
 int muon_abi_version(void);
 
@@ -453,6 +607,52 @@ muon_status muon_act_encode(muon_handle *h, const void *x, int64_t rows, int64_t
                             int32_t dtype, const muon_act8 *q, void *stream);
 muon_status muon_act_decode(muon_handle *h, const muon_act8 *q, void *y, int64_t rows, int64_t cols,
                             int64_t ld_y, int32_t dtype, void *stream);
+
+/* ---- the block operators ----
+ * Conventions, workspaces, capture and errors are those of the seven layer
+ * operators (muon_layernorm_forward). */
+
+/* Gated feed-forward: with zg = x Wg + bias_gate and zu = x Wu + bias_up,
+ *
+ *   h = act(zg) zu
+ *
+ * both products, the activation and the product in one kernel, sums in float32,
+ * h rounded once.  The down projection behind it is muon_linear_forward, its
+ * weight's gradient muon_linear_grad_weight. */
+muon_status muon_gated_forward(muon_handle *h, const muon_gated_args *args, void *stream);
+
+/* With dh = dy Wd^T, the gradient at h through the down projection,
+ *
+ *   dgate = dh zu act'(zg),  dup = dh act(zg),  and h = act(zg) zu again */
+muon_status muon_gated_grad_hidden(muon_handle *h, const muon_gated_grad_hidden_args *args, void *stream);
+
+/* dx = dgate Wg^T + dup Wu^T + add, one sum */
+muon_status muon_gated_grad_input(muon_handle *h, const muon_gated_grad_input_args *args, void *stream);
+
+/* dw_gate = x^T dgate, dw_up = x^T dup (as the weights are stored), db_gate and
+ * db_up the column sums of dgate and dup */
+muon_status muon_gated_grad_weight(muon_handle *h, const muon_gated_grad_weight_args *args, void *stream);
+
+/* y = x under the mask + add.  The gradient at x is the same call on dy. */
+muon_status muon_dropout(muon_handle *h, const muon_dropout_args *args, void *stream);
+
+/* The junction behind a block: with t = norm_post(branch) post_gain + post_bias,
+ *
+ *   s = residual_scale x + branch_scale gate drop(t)     rounded to the stream's type
+ *   y = norm_pre(s) pre_gain + pre_bias                  of s as rounded
+ *
+ * in one pass over the rows.  Without a branch it is the norm before the first
+ * block (residual_scale 1, no post norm, gate or dropout); with pre_norm NONE it
+ * ends behind the last one.  An absent gain or gate is 1, an absent bias 0. */
+muon_status muon_blocknorm_forward(muon_handle *h, const muon_blocknorm_args *args, void *stream);
+
+/* Its gradient: with g = ds + (the gradient of norm_pre at s), e = branch_scale
+ * drop(g), and the branch's normalised rows oh (the branch itself without a post norm),
+ *
+ *   dx = residual_scale g;  dbranch = the gradient of norm_post under e gate post_gain
+ *   dpost_gain = sum e gate oh;  dpost_bias = sum e gate;  dgate = sum e t
+ *   dpre_gain, dpre_bias: as in muon_layernorm_backward */
+muon_status muon_blocknorm_backward(muon_handle *h, const muon_blocknorm_grad_args *args, void *stream);
 
 /* Frobenius norms ||u||_F of the orthogonalised inputs of the most recent
  * muon_step (as enqueued: read after that step's kernels), one per plan entry (a blocked matrix has one per block, row-major)

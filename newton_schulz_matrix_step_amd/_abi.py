@@ -16,7 +16,7 @@ from typing import List, Optional, Sequence
 # the in-tree build; MUON_LIBRARY names another build of the same library to load instead
 LIB_PATH = os.environ.get("MUON_LIBRARY") or os.path.join(os.path.dirname(os.path.abspath(__file__)),
                                                           "libmuon_mi355x.so")
-ABI_VERSION = 7   # the MUON_ABI_VERSION of the header this binding mirrors
+ABI_VERSION = 8   # the MUON_ABI_VERSION of the header this binding mirrors
 
 MUON_OK = 0
 MUON_ERR_INVALID_ARG = 1
@@ -34,6 +34,8 @@ MUON_COMPUTE_FP32 = 1
 MUON_ACT8_GROUP = 32       # columns of a row that share one exponent of an 8-bit checkpoint
 ACTIVATIONS = {"none": 0, "gelu": 1, "relu_sq": 2}        # muon_activation
 W_LAYOUTS = {"in_out": 0, "out_in": 1}                    # muon_weight_layout
+GATES = {"silu": 0, "gelu": 1, "sigmoid": 2, "relu": 3}   # muon_gate
+NORMS = {"none": 0, "rms": 1, "layer": 2}                 # muon_norm
 
 MUON_INIT_PROFILE = 0x1
 MUON_INIT_FAIL_ALLOC = 0x2
@@ -66,6 +68,13 @@ EXPORTED_SYMBOLS = (
     "muon_linear_grad_weight",
     "muon_act_encode",
     "muon_act_decode",
+    "muon_gated_forward",
+    "muon_gated_grad_hidden",
+    "muon_gated_grad_input",
+    "muon_gated_grad_weight",
+    "muon_dropout",
+    "muon_blocknorm_forward",
+    "muon_blocknorm_backward",
     "muon_read_norms",
     "muon_kernel_stats_read",
     "muon_kernel_stats_reset",
@@ -263,6 +272,209 @@ class muon_linear_grad_weight_args(ctypes.Structure):
     ]
 
 
+class muon_gated_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("w_gate", ctypes.c_void_p),
+        ("w_up", ctypes.c_void_p),
+        ("bias_gate", ctypes.c_void_p),
+        ("bias_up", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("up", ctypes.c_void_p),
+        ("gate8", muon_act8),
+        ("up8", muon_act8),
+        ("rows", ctypes.c_int64),
+        ("in_", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_w", ctypes.c_int64),
+        ("ld_h", ctypes.c_int64),
+        ("ld_z", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("bias_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("w_layout", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class muon_gated_grad_hidden_args(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("w_down", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("up", ctypes.c_void_p),
+        ("gate8", muon_act8),
+        ("up8", muon_act8),
+        ("dgate", ctypes.c_void_p),
+        ("dup", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("out", ctypes.c_int64),
+        ("ld_dy", ctypes.c_int64),
+        ("ld_w", ctypes.c_int64),
+        ("ld_z", ctypes.c_int64),
+        ("ld_dz", ctypes.c_int64),
+        ("ld_h", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("w_layout", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class muon_gated_grad_input_args(ctypes.Structure):
+    _fields_ = [
+        ("dgate", ctypes.c_void_p),
+        ("dup", ctypes.c_void_p),
+        ("w_gate", ctypes.c_void_p),
+        ("w_up", ctypes.c_void_p),
+        ("add", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("in_", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("ld_dz", ctypes.c_int64),
+        ("ld_w", ctypes.c_int64),
+        ("ld_add", ctypes.c_int64),
+        ("ld_dx", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("w_layout", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class muon_gated_grad_weight_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("x8", muon_act8),
+        ("dgate", ctypes.c_void_p),
+        ("dup", ctypes.c_void_p),
+        ("dw_gate", ctypes.c_void_p),
+        ("dw_up", ctypes.c_void_p),
+        ("db_gate", ctypes.c_void_p),
+        ("db_up", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("in_", ctypes.c_int64),
+        ("hidden", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_dz", ctypes.c_int64),
+        ("ld_dw", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("dw_dtype", ctypes.c_int32),
+        ("db_dtype", ctypes.c_int32),
+        ("w_layout", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class muon_dropout_mask(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("seed", ctypes.c_uint64),
+        ("offset", ctypes.c_uint64),
+        ("step", ctypes.c_void_p),
+    ]
+
+
+class muon_dropout_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("add", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("drop", muon_dropout_mask),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_add", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class muon_blocknorm_args(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("branch", ctypes.c_void_p),
+        ("post_gain", ctypes.c_void_p),
+        ("post_bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("pre_gain", ctypes.c_void_p),
+        ("pre_bias", ctypes.c_void_p),
+        ("s", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("y8", muon_act8),
+        ("post_mean", ctypes.c_void_p),
+        ("post_rstd", ctypes.c_void_p),
+        ("pre_mean", ctypes.c_void_p),
+        ("pre_rstd", ctypes.c_void_p),
+        ("drop", muon_dropout_mask),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_branch", ctypes.c_int64),
+        ("ld_s", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("residual_scale", ctypes.c_float),
+        ("branch_scale", ctypes.c_float),
+        ("post_eps", ctypes.c_float),
+        ("pre_eps", ctypes.c_float),
+        ("post_norm", ctypes.c_int32),
+        ("pre_norm", ctypes.c_int32),
+        ("stream_dtype", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class muon_blocknorm_grad_args(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p),
+        ("ds", ctypes.c_void_p),
+        ("s", ctypes.c_void_p),
+        ("branch", ctypes.c_void_p),
+        ("post_gain", ctypes.c_void_p),
+        ("post_bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("pre_gain", ctypes.c_void_p),
+        ("post_mean", ctypes.c_void_p),
+        ("post_rstd", ctypes.c_void_p),
+        ("pre_mean", ctypes.c_void_p),
+        ("pre_rstd", ctypes.c_void_p),
+        ("dx", ctypes.c_void_p),
+        ("dbranch", ctypes.c_void_p),
+        ("dpost_gain", ctypes.c_void_p),
+        ("dpost_bias", ctypes.c_void_p),
+        ("dgate", ctypes.c_void_p),
+        ("dpre_gain", ctypes.c_void_p),
+        ("dpre_bias", ctypes.c_void_p),
+        ("drop", muon_dropout_mask),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_dy", ctypes.c_int64),
+        ("ld_ds", ctypes.c_int64),
+        ("ld_s", ctypes.c_int64),
+        ("ld_branch", ctypes.c_int64),
+        ("ld_dx", ctypes.c_int64),
+        ("ld_dbranch", ctypes.c_int64),
+        ("residual_scale", ctypes.c_float),
+        ("branch_scale", ctypes.c_float),
+        ("post_norm", ctypes.c_int32),
+        ("pre_norm", ctypes.c_int32),
+        ("stream_dtype", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("accumulate", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{status_str(status)}: {msg}" if msg else status_str(status))
@@ -301,7 +513,14 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                      ("muon_layernorm_backward", muon_layernorm_grad_args),
                      ("muon_linear_forward", muon_linear_args),
                      ("muon_linear_grad_input", muon_linear_grad_input_args),
-                     ("muon_linear_grad_weight", muon_linear_grad_weight_args)):
+                     ("muon_linear_grad_weight", muon_linear_grad_weight_args),
+                     ("muon_gated_forward", muon_gated_args),
+                     ("muon_gated_grad_hidden", muon_gated_grad_hidden_args),
+                     ("muon_gated_grad_input", muon_gated_grad_input_args),
+                     ("muon_gated_grad_weight", muon_gated_grad_weight_args),
+                     ("muon_dropout", muon_dropout_args),
+                     ("muon_blocknorm_forward", muon_blocknorm_args),
+                     ("muon_blocknorm_backward", muon_blocknorm_grad_args)):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [vp, ctypes.POINTER(st), vp]
@@ -812,6 +1031,242 @@ def muon_act_decode(handle: int, q: Act8, y, stream=None) -> None:
     dc = k.storage("y", y)
     a = k.act8("q", q, y.shape)
     _check(handle, load().muon_act_decode(handle, a, y.data_ptr(), r, c, _ld2(y), dc, k.stream(stream)))
+
+
+def _pair8(k: _Args, gate, up, names):
+    """Whether a pair of pre-activations is 8-bit checkpoints."""
+    g8, u8 = isinstance(gate, Act8), isinstance(up, Act8)
+    if g8 != u8 or (gate is None) != (up is None):
+        k.fail(f"{names[0]} and {names[1]} must be both tensors or both Act8")
+    return g8
+
+
+def _same_ld(k: _Args, names, a: int, b: int, ta, tb) -> int:
+    """The leading dimension that both tensors of a pair have (one row takes any)."""
+    if a != b and ta is not None and tb is not None:
+        if ta.shape[0] > 1:
+            k.fail(f"{names[0]} and {names[1]} must have one leading dimension, got {a} and {b}")
+        return max(a, b)
+    return a
+
+
+def _pair(k: _Args, names, ta, tb, shape, dt, like):
+    """(pointer, pointer, leading dimension) of a pair of matrices."""
+    pa, la = k.matrix(names[0], ta, shape, dt, like)
+    pb, lb = k.matrix(names[1], tb, shape, dt, like)
+    return pa, pb, la if la == lb else _same_ld(k, names, la, lb, ta, tb)
+
+
+def muon_gated_forward(handle: int, x, w_gate, w_up, h, bias_gate=None, bias_up=None, act: str = "silu",
+                       gate_out=None, up_out=None, w_layout: str = "in_out", stream=None) -> None:
+    """h = act(x Wg + bias_gate) (x Wu + bias_up); the weights are (in x hidden)
+    or, with ``w_layout`` "out_in", (hidden x in).  ``gate_out`` and ``up_out``
+    (two tensors or two Act8) receive the pre-activations."""
+    k = _Args("muon_gated_forward", x)
+    i, f, lay = _linear_sizes(k, w_gate, w_layout)
+    r = k.rows_cols("x", x)[0]
+    dt, dc, ac = x.dtype, k.storage("x", x), _code(k.what, GATES, act, "act")
+    z8 = _pair8(k, gate_out, up_out, ("gate_out", "up_out"))
+    px, ldx = k.matrix("x", x, (r, i), dt, "x")
+    pg, pu, ldw = _pair(k, ("w_gate", "w_up"), w_gate, w_up, w_gate.shape, dt, "x")
+    ph, ldh = k.matrix("h", h, (r, f), dt, "x")
+    pzg, pzu, ldz = _pair(k, ("gate_out", "up_out"), None if z8 else gate_out, None if z8 else up_out, (r, f), dt, "x")
+    bias = bias_gate if bias_gate is not None else bias_up
+    bc = MUON_F32 if bias is None else k.storage("bias", bias)
+    bt = None if bias is None else bias.dtype
+    a = muon_gated_args(px, pg, pu, k.vector("bias_gate", bias_gate, f, bt), k.vector("bias_up", bias_up, f, bt, "bias_gate"),
+                        ph, pzg, pzu, k.act8("gate_out", gate_out if z8 else None, (r, f)),
+                        k.act8("up_out", up_out if z8 else None, (r, f)), r, i, f, ldx, ldw, ldh, ldz, dc, bc, ac, lay, 0)
+    _check(handle, load().muon_gated_forward(handle, a, k.stream(stream)))
+
+
+def muon_gated_grad_hidden(handle: int, dy, w_down, gate, up, dgate, dup, act: str = "silu", h_out=None,
+                           w_layout: str = "in_out", stream=None) -> None:
+    """From dh = dy Wd^T: dgate = dh up act'(gate) and dup = dh act(gate); ``gate``
+    and ``up`` are the forward pass's pre-activations (two tensors or two Act8),
+    ``w_down`` is (hidden x out) or (out x hidden), ``h_out`` receives act(gate) up."""
+    k = _Args("muon_gated_grad_hidden", dy)
+    f, o, lay = _linear_sizes(k, w_down, w_layout)
+    r = k.rows_cols("dy", dy)[0]
+    dt, dc, ac = dy.dtype, k.storage("dy", dy), _code(k.what, GATES, act, "act")
+    z8 = _pair8(k, gate, up, ("gate", "up"))
+    pdy, lddy = k.matrix("dy", dy, (r, o), dt, "dy")
+    pw, ldw = k.matrix("w_down", w_down, w_down.shape, dt, "dy")
+    pzg, pzu, ldz = _pair(k, ("gate", "up"), None if z8 else gate, None if z8 else up, (r, f), dt, "dy")
+    pdg, pdu, lddz = _pair(k, ("dgate", "dup"), dgate, dup, (r, f), dt, "dy")
+    ph, ldh = k.matrix("h_out", h_out, (r, f), dt, "dy")
+    a = muon_gated_grad_hidden_args(pdy, pw, pzg, pzu, k.act8("gate", gate if z8 else None, (r, f)),
+                                    k.act8("up", up if z8 else None, (r, f)), pdg, pdu, ph, r, f, o, lddy, ldw, ldz, lddz,
+                                    ldh, dc, ac, lay, 0)
+    _check(handle, load().muon_gated_grad_hidden(handle, a, k.stream(stream)))
+
+
+def muon_gated_grad_input(handle: int, dgate, dup, w_gate, w_up, dx, add=None, w_layout: str = "in_out",
+                          stream=None) -> None:
+    """dx = dgate Wg^T + dup Wu^T + ``add`` (which may be ``dx``)."""
+    k = _Args("muon_gated_grad_input", dgate)
+    i, f, lay = _linear_sizes(k, w_gate, w_layout)
+    r = k.rows_cols("dgate", dgate)[0]
+    dt, dc = dgate.dtype, k.storage("dgate", dgate)
+    pdg, pdu, lddz = _pair(k, ("dgate", "dup"), dgate, dup, (r, f), dt, "dgate")
+    pg, pu, ldw = _pair(k, ("w_gate", "w_up"), w_gate, w_up, w_gate.shape, dt, "dgate")
+    pa, lda = k.matrix("add", add, (r, i), dt, "dgate")
+    pdx, lddx = k.matrix("dx", dx, (r, i), dt, "dgate")
+    a = muon_gated_grad_input_args(pdg, pdu, pg, pu, pa, pdx, r, i, f, lddz, ldw, lda, lddx, dc, lay, 0)
+    _check(handle, load().muon_gated_grad_input(handle, a, k.stream(stream)))
+
+
+def muon_gated_grad_weight(handle: int, x, dgate, dup, dw_gate, dw_up, db_gate=None, db_up=None,
+                           accumulate: bool = False, w_layout: str = "in_out", stream=None) -> None:
+    """dw_gate = x^T dgate and dw_up = x^T dup (stored as the weights are), db_gate
+    and db_up their column sums; ``x`` is a tensor or an Act8, ``accumulate`` adds
+    to all four."""
+    k = _Args("muon_gated_grad_weight", dgate)
+    i, f, lay = _linear_sizes(k, dw_gate, w_layout)
+    r = k.rows_cols("dgate", dgate)[0]
+    dt, dc, wc = dgate.dtype, k.storage("dgate", dgate), k.storage("dw_gate", dw_gate)
+    x8 = x if isinstance(x, Act8) else None
+    px, ldx = k.matrix("x", None if x8 is not None else x, (r, i), dt, "dgate")
+    pdg, pdu, lddz = _pair(k, ("dgate", "dup"), dgate, dup, (r, f), dt, "dgate")
+    pwg, pwu, lddw = _pair(k, ("dw_gate", "dw_up"), dw_gate, dw_up, dw_gate.shape, dw_gate.dtype, "dw_gate")
+    db = db_gate if db_gate is not None else db_up
+    bc = MUON_F32 if db is None else k.storage("db", db)
+    bt = None if db is None else db.dtype
+    a = muon_gated_grad_weight_args(px, k.act8("x", x8, (r, i)), pdg, pdu, pwg, pwu, k.vector("db_gate", db_gate, f, bt),
+                                    k.vector("db_up", db_up, f, bt, "db_gate"), r, i, f, ldx, lddz, lddw, dc, wc, bc, lay,
+                                    1 if accumulate else 0, 0)
+    _check(handle, load().muon_gated_grad_weight(handle, a, k.stream(stream)))
+
+
+class Dropout:
+    """A dropout mask: the probability ``p`` of dropping, the generator's ``seed``
+    and ``offset`` (integers mod 2^64).  ``step``, an int64 tensor of one element on
+    the GPU, is added to the offset when the kernel runs (a captured graph draws a
+    new mask whenever the program counts it up)."""
+
+    __slots__ = ("p", "seed", "offset", "step")
+
+    def __init__(self, p: float, seed: int, offset: int = 0, step=None):
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"Dropout: p must lie in 0..1, got {p}")
+        if step is not None:
+            import torch
+            if step.dtype is not torch.int64 or step.numel() != 1:
+                raise ValueError("Dropout: step must be an int64 tensor of one element")
+        self.p, self.seed, self.offset, self.step = float(p), int(seed), int(offset), step
+
+    def _c(self, k: _Args) -> muon_dropout_mask:
+        step = None
+        if self.step is not None:
+            if self.step.get_device() != k.device:
+                k.device_ok = False
+            step = self.step.data_ptr()
+        m = 0xFFFFFFFFFFFFFFFF
+        return muon_dropout_mask(self.p, 0, self.seed & m, self.offset & m, step)
+
+
+_NO_DROPOUT = muon_dropout_mask()
+
+
+def muon_dropout(handle: int, x, y, drop: Dropout, add=None, stream=None) -> None:
+    """y = x under the mask + ``add``; ``y`` may be ``x`` or ``add``.  The gradient
+    at x is the same call on dy."""
+    k = _Args("muon_dropout", x)
+    shape = k.rows_cols("x", x)
+    r, c = shape
+    dt, dc = x.dtype, k.storage("x", x)
+    px, ldx = k.matrix("x", x, shape, dt, "x")
+    py, ldy = k.matrix("y", y, shape, dt, "x")
+    pa, lda = k.matrix("add", add, shape, dt, "x")
+    a = muon_dropout_args(px, pa, py, drop._c(k), r, c, ldx, lda, ldy, dc, 0)
+    _check(handle, load().muon_dropout(handle, a, k.stream(stream)))
+
+
+def _param_type(k: _Args, named):
+    """(dtype, muon_dtype) that all given parameters have."""
+    dt = None
+    for nm, t in named:
+        if t is None:
+            continue
+        if dt is None:
+            dt = t.dtype
+            c = k.storage(nm, t)
+        elif t.dtype is not dt:
+            k.fail(f"{nm} is {t.dtype}, {named[0][0]} and the other parameters {dt}")
+    return (None, MUON_F32) if dt is None else (dt, c)
+
+
+def muon_blocknorm_forward(handle: int, x, branch=None, s=None, y=None, post_norm: str = "none", post_gain=None,
+                           post_bias=None, gate=None, pre_norm: str = "none", pre_gain=None, pre_bias=None,
+                           residual_scale: float = 1.0, branch_scale: float = 1.0, drop: Optional[Dropout] = None,
+                           post_eps: float = 1e-5, pre_eps: float = 1e-5, post_mean=None, post_rstd=None, pre_mean=None,
+                           pre_rstd=None, y8: Optional[Act8] = None, stream=None) -> None:
+    """The junction behind a block: s = residual_scale x + branch_scale gate
+    drop(post_norm(branch)) and y = pre_norm(s), norms "none", "rms" or "layer".
+    ``s`` may be ``x``; without ``branch`` there is no ``s``, and with ``pre_norm``
+    "none" no ``y``.  Statistics (float32, one per row) and ``y8`` (y's 8-bit
+    checkpoint) are written where given."""
+    k = _Args("muon_blocknorm_forward", x)
+    shape = k.rows_cols("x", x)
+    r, c = shape
+    st, sc = x.dtype, k.storage("x", x)
+    block = branch if branch is not None else y
+    dt, dc = (st, sc) if block is None else (block.dtype, k.storage("branch" if branch is not None else "y", block))
+    pt, pc = _param_type(k, (("post_gain", post_gain), ("post_bias", post_bias), ("gate", gate), ("pre_gain", pre_gain),
+                             ("pre_bias", pre_bias)))
+    f32 = k.torch.f32
+    px, ldx = k.matrix("x", x, shape, st, "x")
+    pb, ldb = k.matrix("branch", branch, shape, dt, "branch")
+    ps, lds = k.matrix("s", s, shape, st, "x")
+    py, ldy = k.matrix("y", y, shape, dt, "branch")
+    v = k.vector
+    a = muon_blocknorm_args(px, pb, v("post_gain", post_gain, c, pt), v("post_bias", post_bias, c, pt), v("gate", gate, c, pt),
+                            v("pre_gain", pre_gain, c, pt), v("pre_bias", pre_bias, c, pt), ps, py, k.act8("y8", y8, shape),
+                            v("post_mean", post_mean, r, f32), v("post_rstd", post_rstd, r, f32),
+                            v("pre_mean", pre_mean, r, f32), v("pre_rstd", pre_rstd, r, f32),
+                            _NO_DROPOUT if drop is None else drop._c(k), r, c, ldx, ldb, lds, ldy, residual_scale,
+                            branch_scale, post_eps, pre_eps, _code(k.what, NORMS, post_norm, "post_norm"),
+                            _code(k.what, NORMS, pre_norm, "pre_norm"), sc, dc, pc, 0)
+    _check(handle, load().muon_blocknorm_forward(handle, a, k.stream(stream)))
+
+
+def muon_blocknorm_backward(handle: int, dx, ds=None, dy=None, s=None, branch=None, dbranch=None, post_norm: str = "none",
+                            post_gain=None, post_bias=None, gate=None, post_mean=None, post_rstd=None,
+                            pre_norm: str = "none", pre_gain=None, pre_mean=None, pre_rstd=None,
+                            residual_scale: float = 1.0, branch_scale: float = 1.0, drop: Optional[Dropout] = None,
+                            dpost_gain=None, dpost_bias=None, dgate=None, dpre_gain=None, dpre_bias=None,
+                            accumulate: bool = False, stream=None) -> None:
+    """dx, dbranch and the parameters' gradients of a junction from ``ds`` (the
+    gradient at the stream behind it; may be ``dx``) and ``dy`` (at y).  ``s`` is
+    that stream (the forward pass's x without a branch)."""
+    k = _Args("muon_blocknorm_backward", dx)
+    shape = k.rows_cols("dx", dx)
+    r, c = shape
+    st, sc = dx.dtype, k.storage("dx", dx)
+    nm, block = next(((n, t) for n, t in (("dy", dy), ("branch", branch), ("dbranch", dbranch)) if t is not None), ("", None))
+    dt, dc = (st, sc) if block is None else (block.dtype, k.storage(nm, block))
+    pt, pc = _param_type(k, (("post_gain", post_gain), ("post_bias", post_bias), ("gate", gate), ("pre_gain", pre_gain),
+                             ("dpost_gain", dpost_gain), ("dpost_bias", dpost_bias), ("dgate", dgate),
+                             ("dpre_gain", dpre_gain), ("dpre_bias", dpre_bias)))
+    f32 = k.torch.f32
+    pdy, lddy = k.matrix("dy", dy, shape, dt, nm)
+    pds, ldds = k.matrix("ds", ds, shape, st, "dx")
+    ps, lds = k.matrix("s", s, shape, st, "dx")
+    pb, ldb = k.matrix("branch", branch, shape, dt, nm)
+    pdx, lddx = k.matrix("dx", dx, shape, st, "dx")
+    pdb, lddb = k.matrix("dbranch", dbranch, shape, dt, nm)
+    v = k.vector
+    a = muon_blocknorm_grad_args(pdy, pds, ps, pb, v("post_gain", post_gain, c, pt), v("post_bias", post_bias, c, pt),
+                                 v("gate", gate, c, pt), v("pre_gain", pre_gain, c, pt),
+                                 v("post_mean", post_mean, r, f32), v("post_rstd", post_rstd, r, f32),
+                                 v("pre_mean", pre_mean, r, f32), v("pre_rstd", pre_rstd, r, f32), pdx, pdb,
+                                 v("dpost_gain", dpost_gain, c, pt), v("dpost_bias", dpost_bias, c, pt),
+                                 v("dgate", dgate, c, pt), v("dpre_gain", dpre_gain, c, pt),
+                                 v("dpre_bias", dpre_bias, c, pt), _NO_DROPOUT if drop is None else drop._c(k), r, c, lddy,
+                                 ldds, lds, ldb, lddx, lddb, residual_scale, branch_scale,
+                                 _code(k.what, NORMS, post_norm, "post_norm"), _code(k.what, NORMS, pre_norm, "pre_norm"),
+                                 sc, dc, pc, 1 if accumulate else 0, 0)
+    _check(handle, load().muon_blocknorm_backward(handle, a, k.stream(stream)))
 
 
 def muon_read_norms(handle: int, n: int, stream=None) -> List[float]:

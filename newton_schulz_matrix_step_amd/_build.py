@@ -22,7 +22,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 ARCH = "gfx950"
 
 SOURCES = ["muon_api.cpp", "muon_kernels.hip", "adamw_kernels.hip", "muon_static.hip",
-           "layer_api.cpp", "norm_kernels.hip", "linear_kernels.hip"]
+           "layer_api.cpp", "norm_kernels.hip", "linear_kernels.hip", "block_api.cpp", "gated_kernels.hip",
+           "blocknorm_kernels.hip", "blocknorm_grad_kernels.hip", "dropout_kernels.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -42,7 +43,7 @@ COMMON_FLAGS = [
 # accumulators of the linear products stay in VGPRs: where the register budget
 # would allow the accumulation registers as well, the main loops fill up with
 # copies between the two files
-EXTRA_FLAGS = {"linear_kernels.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+EXTRA_FLAGS = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in ("linear_kernels.hip", "gated_kernels.hip")}
 
 
 def _hipcc() -> str:

@@ -1,0 +1,190 @@
+// gfx950 kernels of the gated feed-forward's products:
+//
+//   forward          zg = x Wg + bg, zu = x Wu + bu, h = act(zg) zu   (zg, zu kept, also in 8 bits)
+//   hidden gradient  dh = dy Wd^T, dzg = dh zu act'(zg), dzu = dh act(zg)   (h written beside them)
+//   input gradient   dx = dzg Wg^T + dzu Wu^T + add
+//   weight gradient  dWg = x^T dzg, dWu = x^T dzu, column sums dbg, dbu
+//
+// Each is one launch of the tile kernels of linear_device.hpp: the forward's
+// tiles hold the same columns of both projections, so that a lane has both
+// sums of its elements; the input gradient is one sum over twice the k; the
+// weight gradient's tiles are both outputs'.  Sums are float32, every result is
+// rounded once.
+
+#include "linear_device.hpp"
+
+namespace muon {
+namespace {
+
+// The splits' sums, added in order, through the epilogue: 8 elements a lane.
+// blockIdx.y is the output of a PAIR_OUT call; the workgroups past the output's
+// join the column sums.
+__device__ __forceinline__ void add_partial(const GMEM float* p, int64_t step, int splits, float (&v)[8]) {
+    for (int s = 0; s < splits; ++s, p += step) {
+        const f32x4_t x = *reinterpret_cast<const GMEM f32x4_t*>(p);
+        const f32x4_t y = *reinterpret_cast<const GMEM f32x4_t*>(p + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] += x[k];
+            v[4 + k] += y[k];
+        }
+    }
+}
+__global__ __launch_bounds__(256) void gated_join_kernel(GatedArgs a, int64_t out_blocks) {
+    const OutShape o = out_shape(a);
+    const int64_t one = o.rows * o.ldp;                  // elements of a split's sums
+    if (blockIdx.y) {
+        a.out = a.out2;
+        a.db = a.db2;
+        a.partial += a.splits * one;
+        if (a.db_partial) a.db_partial += a.splits * a.N;
+    }
+    if (int64_t(blockIdx.x) >= out_blocks) {
+        const int64_t n = (int64_t(blockIdx.x) - out_blocks) * 256 + threadIdx.x;
+        if (n >= a.N || !a.db) return;
+        float v = 0.f;
+        for (int s = 0; s < a.splits; ++s) v += gm(a.db_partial)[int64_t(s) * a.N + n];
+        if (a.accumulate) v += load1(a.db, n, a.db_dt);
+        store1(a.db, n, a.db_dt, v);
+        return;
+    }
+    const int64_t rpr = o.ldp / 8;                       // runs per row, a multiple of 4
+    const int64_t idx = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t r = idx / rpr, c = (idx % rpr) * 8;
+    int64_t n = o.cols - c;
+    n = r < o.rows ? (n > 8 ? 8 : n) : 0;
+    const int nv = n > 0 ? int(n) : 0;
+    float v[8], u[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = u[k] = 0.f;
+    const GMEM float* p = gm(a.partial) + r * o.ldp + c;
+    if (a.pair == PAIR_COLS) {
+        if (nv) {
+            add_partial(p, 2 * one, a.splits, v);
+            add_partial(p + one, 2 * one, a.splits, u);
+        }
+        gated_any(a, r, c, nv, v, u);
+    } else {
+        if (nv) add_partial(p, one, a.splits, v);
+        run_any(a, r, c, nv, v);
+    }
+}
+
+int64_t tiles_of(const GatedArgs& a, int edge) {
+    const int64_t ce = a.pair == PAIR_COLS ? edge / 2 : edge;
+    return ((a.M + edge - 1) / edge) * ((a.N + ce - 1) / ce) * (a.pair == PAIR_OUT ? 2 : 1);
+}
+
+template <class T, bool AKC, bool BKC, int KIND, bool TR, int PAIR>
+hipError_t launch_tile(const GatedArgs& a, hipStream_t s) {
+    const dim3 grid(unsigned((tiles_of(a, a.tile) * a.splits + 7) / 8 * 8)), block(256);
+    if (a.tile == 64 && a.deep)
+        hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, S_DMA, S_DMA, KIND, TR, 64, 8, PAIR>), grid, block, 0, s, a);
+    else if (a.tile == 64)
+        hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, S_DMA, S_DMA, KIND, TR, 64, 4, PAIR>), grid, block, 0, s, a);
+    else if (a.deep)
+        hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, S_DMA, S_DMA, KIND, TR, 128, 4, PAIR>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((linear_tile_kernel<T, AKC, BKC, S_DMA, S_DMA, KIND, TR, 128, 2, PAIR>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+template <bool AKC, bool BKC, int KIND, bool TR, int PAIR>
+hipError_t launch_kernel(const GatedArgs& a, hipStream_t s) {
+    if (a.tile == 256) {
+        const dim3 grid(unsigned((tiles_of(a, 256) * a.splits + 7) / 8 * 8));
+        hipLaunchKernelGGL((linear_pp_kernel<AKC, BKC, KIND, TR, PAIR>), grid, dim3(kPpThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    return a.dt == 0 ? launch_tile<uint16_t, AKC, BKC, KIND, TR, PAIR>(a, s)
+                     : launch_tile<float, AKC, BKC, KIND, TR, PAIR>(a, s);
+}
+
+}  // namespace
+
+int64_t gated_tiles128(const GatedArgs& a) { return tiles_of(a, 128); }
+
+// Tile, split and re-laying by the linear products' time model, for the one
+// product of the same work: twice the columns, twice the k or two outputs.
+GatedPlan plan_gated(GatedArgs& a) {
+    const int64_t bk = a.dt == 0 ? 64 : 32;
+    LinArgs q = a;
+    if (a.pair == PAIR_K) q.K = 2 * ((a.K + bk - 1) / bk) * bk;   // each part ends with a block of its own
+    else if (a.pair != PAIR_NONE) q.N = 2 * a.N;
+    if (a.kind == LIN_GATED_DH) q.kind = LIN_DX;
+    if (a.kind == LIN_GATED) q.kind = LIN_FWD;
+    const LinPlan p = plan_linear(q, true);
+    a.tile = p.tile;
+    a.splits = p.splits;
+    a.deep = tiles_of(a, a.tile) * a.splits <= 256;
+    // leading dimensions of the re-laid operands (the plan's, but for K's rounding)
+    const int64_t chunk = a.dt == 0 ? 8 : 4, es = a.dt == 0 ? 2 : 4;
+    const int64_t ar = a.a_kc ? a.M : a.K, ac = a.a_kc ? a.K : a.M, br = a.b_kc ? a.N : a.K, bc = a.b_kc ? a.K : a.N;
+    a.a_ld = a.a_dma ? 0 : (ac + chunk - 1) / chunk * chunk;
+    a.b_ld = a.b_dma ? 0 : (bc + chunk - 1) / chunk * chunk;
+    GatedPlan g;
+    g.a_bytes = size_t(a.a_ld) * size_t(ar) * size_t(es);
+    g.b_bytes = size_t(a.b_ld) * size_t(br) * size_t(es);
+    if (a.splits > 1) {
+        const OutShape o = out_shape(a);
+        const size_t outs = a.pair == PAIR_COLS || a.pair == PAIR_OUT ? 2 : 1;
+        g.partial_bytes = outs * size_t(a.splits) * size_t(o.rows) * size_t(o.ldp) * 4;
+        g.db_bytes = a.db || a.db2 ? outs * size_t(a.splits) * size_t(a.N) * 4 : 0;
+    }
+    return g;
+}
+
+hipError_t launch_gated(const GatedArgs& args, hipStream_t s) {
+    GatedArgs a = args;
+    if (a.M <= 0 || a.N <= 0) return hipSuccess;
+    const int64_t ar = a.a_kc ? a.M : a.K, ac = a.a_kc ? a.K : a.M, br = a.b_kc ? a.N : a.K, bc = a.b_kc ? a.K : a.N;
+    hipError_t e = hipSuccess;
+    if (a.a_ld) {        // operands with rows of whole aligned chunks, in the workspace
+        if (a.a_exps) {
+            Act8Args q;
+            q.x = nullptr;
+            q.y = a.a_ws;
+            q.q = Act8View{static_cast<int8_t*>(const_cast<void*>(a.a)), const_cast<uint8_t*>(a.a_exps), a.lda,
+                           a.lda_exps, a.a8_vec};
+            q.rows = ar;
+            q.ld = a.a_ld;
+            q.cols = int32_t(ac);
+            q.dt = a.dt;
+            q.vec = a.a8_vec;
+            e = launch_act8_decode(q, s);
+        } else {
+            e = launch_pack(a.a, a.lda, a.a_ws, a.a_ld, ar, ac, a.dt, s);
+            if (e == hipSuccess && a.pair == PAIR_K) e = launch_pack(a.a2, a.lda, a.a2_ws, a.a_ld, ar, ac, a.dt, s);
+        }
+        if (e != hipSuccess) return e;
+        a.a = a.a_ws;
+        a.a2 = a.a2_ws;
+        a.lda = a.a_ld;
+    }
+    if (a.b_ld) {
+        e = launch_pack(a.b, a.ldb, a.b_ws, a.b_ld, br, bc, a.dt, s);
+        if (e == hipSuccess && a.pair != PAIR_NONE) e = launch_pack(a.b2, a.ldb, a.b2_ws, a.b_ld, br, bc, a.dt, s);
+        if (e != hipSuccess) return e;
+        a.b = a.b_ws;
+        a.b2 = a.b2_ws;
+        a.ldb = a.b_ld;
+    }
+    if (a.pair == PAIR_COLS)
+        e = a.b_kc ? launch_kernel<true, true, LIN_GATED, false, PAIR_COLS>(a, s)
+                   : launch_kernel<true, false, LIN_GATED, false, PAIR_COLS>(a, s);
+    else if (a.pair == PAIR_K)
+        e = a.b_kc ? launch_kernel<true, true, LIN_DX, false, PAIR_K>(a, s)
+                   : launch_kernel<true, false, LIN_DX, false, PAIR_K>(a, s);
+    else if (a.pair == PAIR_OUT)
+        e = a.out_trans ? launch_kernel<false, false, LIN_DW, true, PAIR_OUT>(a, s)
+                        : launch_kernel<false, false, LIN_DW, false, PAIR_OUT>(a, s);
+    else
+        e = a.b_kc ? launch_kernel<true, true, LIN_GATED_DH, false, PAIR_NONE>(a, s)
+                   : launch_kernel<true, false, LIN_GATED_DH, false, PAIR_NONE>(a, s);
+    if (e != hipSuccess || a.splits <= 1) return e;
+    const OutShape o = out_shape(a);
+    const int64_t ob = (o.rows * (o.ldp / 8) + 255) / 256, db = a.db || a.db2 ? (a.N + 255) / 256 : 0;
+    hipLaunchKernelGGL(gated_join_kernel, dim3(unsigned(ob + db), a.pair == PAIR_OUT ? 2u : 1u), dim3(256), 0, s, a, ob);
+    return hipGetLastError();
+}
+
+}  // namespace muon

@@ -101,8 +101,56 @@ struct Act8Args {
 hipError_t launch_act8_encode(const Act8Args& a, hipStream_t s);
 hipError_t launch_act8_decode(const Act8Args& a, hipStream_t s);
 
+// ---- dropout (dropout_kernels.hip) ----
+// The mask as the kernels take it: 16 bits an element, dropped under `cut`.
+struct DropMask {
+    uint64_t seed, offset;
+    const uint64_t* step;      // may be null
+    uint32_t cut;              // 0 .. 65536
+    float scale;               // of what is kept
+};
+struct DropoutArgs {
+    const void* x;
+    const void* add;           // may be null
+    void* y;
+    DropMask drop;
+    int64_t rows, ld_x, ld_add, ld_y, row0;   // row0: of a slice of the rows
+    int32_t cols, dt;
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s);
+
+// ---- norms around a block (blocknorm_kernels.hip, blocknorm_grad_kernels.hip) ----
+enum NormKind : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
+struct BlockNormArgs {
+    const void *x, *branch, *post_gain, *post_bias, *gate, *pre_gain, *pre_bias;
+    void *s, *y;
+    Act8View y8;
+    float *post_mean, *post_rstd, *pre_mean, *pre_rstd;
+    DropMask drop;
+    int64_t rows, ld_x, ld_branch, ld_s, ld_y;
+    float alpha, beta, post_eps, pre_eps;
+    int32_t cols, post, pre;
+    int32_t sdt, dt, pdt;      // stream; branch and y; parameters
+};
+struct BlockNormGradArgs {
+    const void *dy, *ds, *s, *branch, *post_gain, *post_bias, *gate, *pre_gain;
+    const float *post_mean, *post_rstd, *pre_mean, *pre_rstd;
+    void *dx, *dbranch, *dpost_gain, *dpost_bias, *dgate, *dpre_gain, *dpre_bias;
+    float* partial;            // [4][parts][cols]: sums of dy xh, dy, e oh, e (those that are wanted)
+    DropMask drop;
+    int64_t rows, ld_dy, ld_ds, ld_s, ld_branch, ld_dx, ld_dbranch;
+    float alpha, beta;
+    int32_t cols, post, pre, parts;
+    int32_t sdt, dt, pdt, accumulate;
+    int32_t at[4];             // place of each sum in `partial`, -1: not wanted
+    int32_t sums;              // how many are
+};
+int blocknorm_parts(int64_t rows, int cols);   // rows of partial sums
+hipError_t launch_blocknorm(const BlockNormArgs& a, hipStream_t s);
+hipError_t launch_blocknorm_grad(const BlockNormGradArgs& a, hipStream_t s);
+
 // ---- the linear layer's products (linear_kernels.hip) ----
-enum LinKind : int { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2 };
+enum LinKind : int { LIN_FWD = 0, LIN_DX = 1, LIN_DW = 2, LIN_GATED = 3, LIN_GATED_DH = 4 };   // epilogues
 enum LinAct : int { ACT_NONE = 0, ACT_GELU = 1, ACT_RELU_SQ = 2 };
 
 // C (M x N) = A B over k.  A (m, k) at a[m * lda + k] (a_kc) or a[k * lda + m];
@@ -159,7 +207,43 @@ struct LinPlan {
     int64_t a_ld = 0, b_ld = 0;
     size_t partial_bytes = 0, db_bytes = 0, a_bytes = 0, b_bytes = 0;
 };
-LinPlan plan_linear(const LinArgs& a);
+// relay_only: operands without whole aligned chunks are always re-laid.
+LinPlan plan_linear(const LinArgs& a, bool relay_only = false);
 hipError_t launch_linear(const LinArgs& a, hipStream_t s);
+// A copy of a matrix with rows of whole aligned 16-byte chunks, their ends zero.
+hipError_t launch_pack(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int64_t cols, int dt,
+                       hipStream_t s);
+
+// ---- the gated feed-forward's products (gated_kernels.hip) ----
+enum GateAct : int { GATE_SILU = 0, GATE_GELU = 1, GATE_SIGMOID = 2, GATE_RELU = 3 };
+
+// How two products of one shape share a launch: the gate's and the up
+// projection's columns side by side in a tile; the sum of two products over k;
+// the tiles of two outputs.
+enum Pair : int { PAIR_NONE = 0, PAIR_COLS = 1, PAIR_K = 2, PAIR_OUT = 3 };
+
+// The second of each pair of tensors.  Both have the leading dimensions, types
+// and alignment flags that LinArgs holds; M, N and K are one product's, and
+// `splits` counts over both parts of a PAIR_K sum.  PAIR_COLS keeps its sums as
+// [splits][gate, up][rows][cols], PAIR_OUT as [output][splits][rows][cols].
+struct GatedArgs : LinArgs {
+    int32_t pair, gate_act;
+    const void* a2;            // PAIR_K
+    const void* b2;
+    const void* bias2;         // LIN_GATED
+    void* z2;                  // the up projection's pre-activation: written (LIN_GATED) or read (LIN_GATED_DH)
+    Act8View z8_2;
+    void* out2;                // PAIR_OUT; LIN_GATED_DH: its gradient
+    void* db2;
+    void* a2_ws;
+    void* b2_ws;
+};
+// Fills a.tile, a.splits, a.deep, a.a_ld and a.b_ld; the bytes of each buffer.
+struct GatedPlan {
+    size_t partial_bytes = 0, db_bytes = 0, a_bytes = 0, b_bytes = 0;   // a, b: of one operand
+};
+GatedPlan plan_gated(GatedArgs& a);
+int64_t gated_tiles128(const GatedArgs& a);   // output tiles of the widest grid
+hipError_t launch_gated(const GatedArgs& a, hipStream_t s);
 
 }  // namespace muon
