@@ -1041,20 +1041,13 @@ def _pair8(k: _Args, gate, up, names):
     return g8
 
 
-def _same_ld(k: _Args, names, a: int, b: int, ta, tb) -> int:
-    """The leading dimension that both tensors of a pair have (one row takes any)."""
-    if a != b and ta is not None and tb is not None:
-        if ta.shape[0] > 1:
-            k.fail(f"{names[0]} and {names[1]} must have one leading dimension, got {a} and {b}")
-        return max(a, b)
-    return a
-
-
 def _pair(k: _Args, names, ta, tb, shape, dt, like):
-    """(pointer, pointer, leading dimension) of a pair of matrices."""
+    """(pointer, pointer, leading dimension) of a pair of matrices (of one row: any)."""
     pa, la = k.matrix(names[0], ta, shape, dt, like)
     pb, lb = k.matrix(names[1], tb, shape, dt, like)
-    return pa, pb, la if la == lb else _same_ld(k, names, la, lb, ta, tb)
+    if la != lb and pa is not None and pb is not None:
+        k.fail(f"{names[0]} and {names[1]} must have one leading dimension, got {la} and {lb}")
+    return pa, pb, la
 
 
 def muon_gated_forward(handle: int, x, w_gate, w_up, h, bias_gate=None, bias_up=None, act: str = "silu",
@@ -1182,18 +1175,12 @@ def muon_dropout(handle: int, x, y, drop: Dropout, add=None, stream=None) -> Non
     _check(handle, load().muon_dropout(handle, a, k.stream(stream)))
 
 
-def _param_type(k: _Args, named):
-    """(dtype, muon_dtype) that all given parameters have."""
-    dt = None
-    for nm, t in named:
-        if t is None:
-            continue
-        if dt is None:
-            dt = t.dtype
-            c = k.storage(nm, t)
-        elif t.dtype is not dt:
-            k.fail(f"{nm} is {t.dtype}, {named[0][0]} and the other parameters {dt}")
-    return (None, MUON_F32) if dt is None else (dt, c)
+def _param_type(k: _Args, *params):
+    """(dtype, muon_dtype) of the first parameter given, which all others must have."""
+    for t in params:
+        if t is not None:
+            return t.dtype, k.storage("a parameter", t)
+    return None, MUON_F32
 
 
 def muon_blocknorm_forward(handle: int, x, branch=None, s=None, y=None, post_norm: str = "none", post_gain=None,
@@ -1212,21 +1199,26 @@ def muon_blocknorm_forward(handle: int, x, branch=None, s=None, y=None, post_nor
     st, sc = x.dtype, k.storage("x", x)
     block = branch if branch is not None else y
     dt, dc = (st, sc) if block is None else (block.dtype, k.storage("branch" if branch is not None else "y", block))
-    pt, pc = _param_type(k, (("post_gain", post_gain), ("post_bias", post_bias), ("gate", gate), ("pre_gain", pre_gain),
-                             ("pre_bias", pre_bias)))
+    pt, pc = _param_type(k, pre_gain, post_gain, gate, pre_bias, post_bias)
     f32 = k.torch.f32
+
+    def par(nm, t):
+        return None if t is None else k.vector(nm, t, c, pt, "another parameter")
+
+    def stat(nm, t):
+        return None if t is None else k.vector(nm, t, r, f32)
+
     px, ldx = k.matrix("x", x, shape, st, "x")
     pb, ldb = k.matrix("branch", branch, shape, dt, "branch")
     ps, lds = k.matrix("s", s, shape, st, "x")
     py, ldy = k.matrix("y", y, shape, dt, "branch")
-    v = k.vector
-    a = muon_blocknorm_args(px, pb, v("post_gain", post_gain, c, pt), v("post_bias", post_bias, c, pt), v("gate", gate, c, pt),
-                            v("pre_gain", pre_gain, c, pt), v("pre_bias", pre_bias, c, pt), ps, py, k.act8("y8", y8, shape),
-                            v("post_mean", post_mean, r, f32), v("post_rstd", post_rstd, r, f32),
-                            v("pre_mean", pre_mean, r, f32), v("pre_rstd", pre_rstd, r, f32),
-                            _NO_DROPOUT if drop is None else drop._c(k), r, c, ldx, ldb, lds, ldy, residual_scale,
-                            branch_scale, post_eps, pre_eps, _code(k.what, NORMS, post_norm, "post_norm"),
-                            _code(k.what, NORMS, pre_norm, "pre_norm"), sc, dc, pc, 0)
+    a = muon_blocknorm_args(px, pb, par("post_gain", post_gain), par("post_bias", post_bias), par("gate", gate),
+                            par("pre_gain", pre_gain), par("pre_bias", pre_bias), ps, py, k.act8("y8", y8, shape),
+                            stat("post_mean", post_mean), stat("post_rstd", post_rstd), stat("pre_mean", pre_mean),
+                            stat("pre_rstd", pre_rstd), _NO_DROPOUT if drop is None else drop._c(k), r, c, ldx, ldb, lds,
+                            ldy, residual_scale, branch_scale, post_eps, pre_eps,
+                            _code(k.what, NORMS, post_norm, "post_norm"), _code(k.what, NORMS, pre_norm, "pre_norm"), sc,
+                            dc, pc, 0)
     _check(handle, load().muon_blocknorm_forward(handle, a, k.stream(stream)))
 
 
@@ -1245,27 +1237,29 @@ def muon_blocknorm_backward(handle: int, dx, ds=None, dy=None, s=None, branch=No
     st, sc = dx.dtype, k.storage("dx", dx)
     nm, block = next(((n, t) for n, t in (("dy", dy), ("branch", branch), ("dbranch", dbranch)) if t is not None), ("", None))
     dt, dc = (st, sc) if block is None else (block.dtype, k.storage(nm, block))
-    pt, pc = _param_type(k, (("post_gain", post_gain), ("post_bias", post_bias), ("gate", gate), ("pre_gain", pre_gain),
-                             ("dpost_gain", dpost_gain), ("dpost_bias", dpost_bias), ("dgate", dgate),
-                             ("dpre_gain", dpre_gain), ("dpre_bias", dpre_bias)))
+    pt, pc = _param_type(k, pre_gain, post_gain, gate, dpre_bias)
     f32 = k.torch.f32
+
+    def par(nm, t):
+        return None if t is None else k.vector(nm, t, c, pt, "another parameter")
+
+    def stat(nm, t):
+        return None if t is None else k.vector(nm, t, r, f32)
+
     pdy, lddy = k.matrix("dy", dy, shape, dt, nm)
     pds, ldds = k.matrix("ds", ds, shape, st, "dx")
     ps, lds = k.matrix("s", s, shape, st, "dx")
     pb, ldb = k.matrix("branch", branch, shape, dt, nm)
     pdx, lddx = k.matrix("dx", dx, shape, st, "dx")
     pdb, lddb = k.matrix("dbranch", dbranch, shape, dt, nm)
-    v = k.vector
-    a = muon_blocknorm_grad_args(pdy, pds, ps, pb, v("post_gain", post_gain, c, pt), v("post_bias", post_bias, c, pt),
-                                 v("gate", gate, c, pt), v("pre_gain", pre_gain, c, pt),
-                                 v("post_mean", post_mean, r, f32), v("post_rstd", post_rstd, r, f32),
-                                 v("pre_mean", pre_mean, r, f32), v("pre_rstd", pre_rstd, r, f32), pdx, pdb,
-                                 v("dpost_gain", dpost_gain, c, pt), v("dpost_bias", dpost_bias, c, pt),
-                                 v("dgate", dgate, c, pt), v("dpre_gain", dpre_gain, c, pt),
-                                 v("dpre_bias", dpre_bias, c, pt), _NO_DROPOUT if drop is None else drop._c(k), r, c, lddy,
-                                 ldds, lds, ldb, lddx, lddb, residual_scale, branch_scale,
-                                 _code(k.what, NORMS, post_norm, "post_norm"), _code(k.what, NORMS, pre_norm, "pre_norm"),
-                                 sc, dc, pc, 1 if accumulate else 0, 0)
+    a = muon_blocknorm_grad_args(pdy, pds, ps, pb, par("post_gain", post_gain), par("post_bias", post_bias),
+                                 par("gate", gate), par("pre_gain", pre_gain), stat("post_mean", post_mean),
+                                 stat("post_rstd", post_rstd), stat("pre_mean", pre_mean), stat("pre_rstd", pre_rstd), pdx,
+                                 pdb, par("dpost_gain", dpost_gain), par("dpost_bias", dpost_bias), par("dgate", dgate),
+                                 par("dpre_gain", dpre_gain), par("dpre_bias", dpre_bias),
+                                 _NO_DROPOUT if drop is None else drop._c(k), r, c, lddy, ldds, lds, ldb, lddx, lddb,
+                                 residual_scale, branch_scale, _code(k.what, NORMS, post_norm, "post_norm"),
+                                 _code(k.what, NORMS, pre_norm, "pre_norm"), sc, dc, pc, 1 if accumulate else 0, 0)
     _check(handle, load().muon_blocknorm_backward(handle, a, k.stream(stream)))
 
 

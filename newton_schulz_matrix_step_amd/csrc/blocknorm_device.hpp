@@ -88,12 +88,14 @@ __device__ __forceinline__ typename RunRaw<T, V>::vec run_get(const GMEM T* p, i
 #pragma unroll
     for (int k = 0; k < R::W; ++k) w[k] = 0u;
     if (n <= 0) return w;
+    T t[V];                              // one wait for all: past the end the last one again
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-        if (k < n) {
-            if constexpr (sizeof(T) == 2) w[k / 2] |= uint32_t(p[k]) << (16 * (k & 1));
-            else w[k] = __float_as_uint(p[k]);
-        }
+    for (int k = 0; k < V; ++k) t[k] = p[k < n ? k : n - 1];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        if constexpr (sizeof(T) == 2) w[k / 2] |= (k < n ? uint32_t(t[k]) : 0u) << (16 * (k & 1));
+        else w[k] = k < n ? __float_as_uint(t[k]) : 0u;
+    }
     return w;
 }
 template <class T, int V>
@@ -149,11 +151,12 @@ struct BlockRow {
     };
     template <class T, bool STREAM>
     static __device__ __forceinline__ void load(const void* p, int64_t base, int cols, int lane, bool on, Raw<T>& r) {
-        const GMEM T* q = gm(static_cast<const T*>(p)) + base;
+        const GMEM char* q = reinterpret_cast<const GMEM char*>(gm(static_cast<const T*>(p)) + base);
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
+        for (int j = 0; j < C; ++j) {    // a scalar base and a 32-bit offset that stays the same from row to row
             const int c = col(j, lane);
-            r.w[j] = run_get<T, V, STREAM>(q + c, on ? cols - c : 0);
+            r.w[j] = run_get<T, V, STREAM>(reinterpret_cast<const GMEM T*>(q + uint32_t(c) * uint32_t(sizeof(T))),
+                                           on ? cols - c : 0);
         }
     }
     template <class T>
@@ -168,20 +171,38 @@ struct BlockRow {
     }
     template <class T, bool STREAM>
     static __device__ __forceinline__ void store(void* p, int64_t base, int cols, int lane, const Raw<T>& r) {
-        GMEM T* q = gm(static_cast<T*>(p)) + base;
+        GMEM char* q = reinterpret_cast<GMEM char*>(gm(static_cast<T*>(p)) + base);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
             const int c = col(j, lane);
-            run_put<T, V, STREAM>(q + c, cols - c, r.w[j]);
+            run_put<T, V, STREAM>(reinterpret_cast<GMEM T*>(q + uint32_t(c) * uint32_t(sizeof(T))), cols - c, r.w[j]);
+        }
+    }
+    // float32 values of the lane's columns to a row of them
+    static __device__ __forceinline__ void store_f32(GMEM float* p, int cols, int lane, const float (&v)[E]) {
+        GMEM char* q = reinterpret_cast<GMEM char*>(p);
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const int c = col(i / V, lane) + i % V;
+            run_put<float, 4, false>(reinterpret_cast<GMEM float*>(q + uint32_t(c) * 4u), cols - c, run_encode<float, 4>(v + i));
         }
     }
     // a parameter's elements of the lane's columns; `absent` where there is none
     static __device__ __forceinline__ void param(const void* p, int dt, int cols, int lane, float absent, float (&v)[E]) {
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-            const int c = col(j, lane);
+            const int c = col(j, lane), n = cols - c;
+            float* o = v + j * V;
+            if (!p) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) v[j * V + k] = c + k < cols ? (p ? load1(p, c + k, dt) : absent) : 0.f;
+                for (int k = 0; k < V; ++k) o[k] = k < n ? absent : 0.f;
+            } else if (dt == 0) {
+                run_decode<uint16_t, V>(run_get<uint16_t, V, false>(gm(static_cast<const uint16_t*>(p)) + c, n), o);
+            } else {
+#pragma unroll
+                for (int h = 0; h < V; h += 4)
+                    run_decode<float, 4>(run_get<float, 4, false>(gm(static_cast<const float*>(p)) + c + h, n - h), o + h);
+            }
         }
     }
     static __device__ __forceinline__ void mask(const Philox& m, uint32_t row, int lane, float (&v)[E]) {
@@ -190,12 +211,72 @@ struct BlockRow {
     }
 };
 
-// Sums of K values over the NW waves of a row; two halves of `red` in turn.
-template <int NW, int K>
-__device__ __forceinline__ void row_sum_turn(float (&v)[K], float (*red)[kWaves][2], int& turn, int wave) {
-    row_sum<NW, K>(v, red[turn], wave);
-    turn ^= 1;
+// Waves of a workgroup whose rows take NW waves each.
+constexpr int block_waves(int nw) { return nw > 8 ? nw : 8; }
+
+// x + x of the lane N places on in its row of 16 (cyclic).
+template <int N>
+__device__ __forceinline__ float add_ror(float x) {
+#ifdef __HIP__
+    return x + __uint_as_float(uint32_t(__builtin_amdgcn_mov_dpp(int(__float_as_uint(x)), 0x120 + N, 0xF, 0xF, true)));
+#else   // a host build for checking runs one lane at a time
+    return x + x;
+#endif
 }
+// Sum over a wave's lanes in every lane, without LDS: rotations within rows of 16,
+// then swaps of rows.  Each step adds two values in either order, so all lanes
+// hold the same bits.
+__device__ __forceinline__ float wave_total(float v) {
+    v = add_ror<1>(add_ror<2>(add_ror<4>(add_ror<8>(v))));
+    typedef unsigned u2 __attribute__((ext_vector_type(2)));
+    const u2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    const u2 t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(t[0]) + __uint_as_float(t[1]);
+}
+// Sum of N (a power of two up to 16) values that lanes hold in turn: lane i value i mod N.
+template <int N>
+__device__ __forceinline__ float turn_total(float v) {
+    if constexpr (N >= 16) v = add_ror<8>(v);
+    if constexpr (N >= 8) v = add_ror<4>(v);
+    if constexpr (N >= 4) v = add_ror<2>(v);
+    if constexpr (N >= 2) v = add_ror<1>(v);
+    return v;
+}
+
+// Sums over the NW waves of a row: `red` holds K values a wave, its two halves
+// used in turn, so that one barrier a sum is enough.
+template <int NW>
+struct RowSums {
+    float (*red)[2][block_waves(NW)];
+    int wave, turn = 0;
+    // exchange of each wave's K values: lane i gets those of wave i mod NW of its row,
+    // and every lane in `ref` the first wave's last one
+    template <int K>
+    __device__ __forceinline__ void exchange(float (&v)[K], float* ref = nullptr) {
+        if constexpr (NW > 1) {
+            float(*r)[block_waves(NW)] = red[turn];
+            turn ^= 1;
+            if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) r[k][wave] = v[k];
+            }
+            __syncthreads();
+            const int w = wave / NW * NW + int(threadIdx.x % NW);
+#pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = r[k][w];
+            if (ref) *ref = r[K - 1][wave / NW * NW];
+        }
+    }
+    template <int K>
+    __device__ __forceinline__ void operator()(float (&v)[K]) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = wave_total(v[k]);
+        exchange(v);
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = turn_total<NW>(v[k]);
+    }
+};
 
 // The types of a junction, and the widest row each variant holds: NW waves x 64
 // lanes x E elements.
@@ -208,13 +289,14 @@ void pick_types(int sdt, int dt, F&& f) {
 constexpr int kBlockRowCols = 8192;
 template <class F>
 void pick_block_row(int cols, F&& f) {
-    if (cols <= 1024) f(std::integral_constant<int, 1>{});
-    else if (cols <= 2048) f(std::integral_constant<int, 2>{});
-    else if (cols <= 4096) f(std::integral_constant<int, 4>{});
-    else f(std::integral_constant<int, 8>{});
+    if (cols <= 512) f(std::integral_constant<int, 1>{});
+    else if (cols <= 1024) f(std::integral_constant<int, 2>{});
+    else if (cols <= 2048) f(std::integral_constant<int, 4>{});
+    else if (cols <= 4096) f(std::integral_constant<int, 8>{});
+    else f(std::integral_constant<int, 16>{});
 }
-inline int block_row_waves(int cols) { return cols <= 1024 ? 1 : cols <= 2048 ? 2 : cols <= 4096 ? 4 : 8; }
-constexpr int kRowElems = 16;            // elements a lane holds of a row
+inline int block_row_waves(int cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2 : cols <= 2048 ? 4 : cols <= 4096 ? 8 : 16; }
+constexpr int kRowElems = 8;             // elements a lane holds of a row
 template <class ST, class BT>
 constexpr int run_width() { return sizeof(ST) == 2 && sizeof(BT) == 2 ? 8 : 4; }
 

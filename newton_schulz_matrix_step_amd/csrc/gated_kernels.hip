@@ -103,20 +103,81 @@ hipError_t launch_kernel(const GatedArgs& a, hipStream_t s) {
 
 int64_t gated_tiles128(const GatedArgs& a) { return tiles_of(a, 128); }
 
-// Tile, split and re-laying by the linear products' time model, for the one
-// product of the same work: twice the columns, twice the k or two outputs.
+// Tile edge and split: the cheapest by a model of the product's time in us, fitted
+// to the four products at ten sizes each in both weight layouts, bf16, on one
+// MI355X (float32: at eight).  With w workgroups a CU and `per` k blocks of 128
+// bytes a row in each:
+//
+//   edge 64    fixed + (block per + tile) max(w, 1)
+//   edge 128   one + block1 per                           w <= 1 (four LDS stages)
+//              fixed + (block per + tile) w               else
+//   edge 256   ceil(w) (fixed + block per)                `block` grows with the CUs at work (clocks fall)
+//
+// `tile` and `fixed` hold the epilogue, which is what the hidden gradient spends
+// most on: five tensors of its size pass through it.  Both sides, measured:
+// 1024 x 1024 -> 1408 hidden, forward 18.5, 14.8 and 28.1 us on edges 64, 128 and
+// 256; 4096 x 1024 -> 2816, weight gradient 57.9 on 128, 70.9 on 256; 4096 x 4096
+// -> 14336, forward 1004 and 735; 4096 x 1024 -> 1408, hidden gradient 28.5 and
+// 53.5.  A split adds the joining kernel (4 us and its sums' bytes, which the
+// caches hold: 14 us for two splits of 8192 x 1024).
+// Operands without whole aligned chunks are always copied first to rows that have
+// them, 8-bit ones decoded.
+// MUON_LINEAR_EDGE fixes the edge where that tile can serve the call (a host
+// build for bounds checking runs each kernel on small sizes); 0: by the model.
+#ifndef MUON_LINEAR_EDGE
+#define MUON_LINEAR_EDGE 0
+#endif
+struct GatedCost {
+    double fixed64, block64, tile64;
+    double one128, block1_128, fixed128, block128, tile128;
+    double fixed256, block256, grow256;   // a k block's time at half the CUs or fewer, and how it grows to all
+};
+//                                       64               128                        256
+constexpr GatedCost kForwardCost = {4, 0.19, 1.4, 6.5, 0.50, 8, 0.49, 0.55, 14.5, 0.85, 0.7};
+constexpr GatedCost kHiddenCost = {5, 0.20, 2.6, 12, 0.55, 8, 0.55, 9.0, 38, 0.95, 0.9};
+constexpr GatedCost kInputCost = {4, 0.21, 0.8, 4, 0.56, 8, 0.45, 0.5, 13, 0.95, 0.9};
+constexpr GatedCost kWeightCost = {4, 0.24, 1.0, 5, 0.60, 8, 0.55, 0.5, 17, 1.5, 0};
+
+double gated_us(const GatedArgs& a, int edge, double w, double per) {
+    if (a.dt != 0)   // float32: bound by the matrix pipes, a CU's workgroups one after the other
+        return edge == 64 ? 4 + (0.58 * per + 1) * std::ceil(w) : w <= 1 ? 6 + 1.75 * per : 8 + 1.9 * per * w;
+    const GatedCost& c = a.kind == LIN_GATED ? kForwardCost : a.kind == LIN_GATED_DH ? kHiddenCost
+                                               : a.kind == LIN_DX                   ? kInputCost
+                                                                                    : kWeightCost;
+    if (edge == 64) return c.fixed64 + (c.block64 * per + c.tile64) * std::max(w, 1.0);
+    if (edge == 128) return w <= 1 ? c.one128 + c.block1_128 * per : c.fixed128 + (c.block128 * per + c.tile128) * w;
+    double block = c.block256 + c.grow256 * std::max(w / std::ceil(w) - 0.5, 0.0);
+    if (a.a_kc && a.b_kc) block *= 0.93;
+    return std::ceil(w) * (c.fixed256 + block * per);
+}
+
 GatedPlan plan_gated(GatedArgs& a) {
-    const int64_t bk = a.dt == 0 ? 64 : 32;
-    LinArgs q = a;
-    if (a.pair == PAIR_K) q.K = 2 * ((a.K + bk - 1) / bk) * bk;   // each part ends with a block of its own
-    else if (a.pair != PAIR_NONE) q.N = 2 * a.N;
-    if (a.kind == LIN_GATED_DH) q.kind = LIN_DX;
-    if (a.kind == LIN_GATED) q.kind = LIN_FWD;
-    const LinPlan p = plan_linear(q, true);
-    a.tile = p.tile;
-    a.splits = p.splits;
+    const OutShape o = out_shape(a);
+    const int64_t bk = a.dt == 0 ? 64 : 32, nkb = (a.K + bk - 1) / bk * (a.pair == PAIR_K ? 2 : 1);
+    const double outs = a.pair == PAIR_COLS || a.pair == PAIR_OUT ? 2 : 1, ins = a.pair == PAIR_K ? 2 : 1;
+    const double sum_bytes = outs * double(o.rows) * double(o.ldp) * 8;
+    const double bytes_us = (ins * double(a.M) * double(a.K) + (a.pair == PAIR_NONE ? 1 : 2) * double(a.K) * double(a.N)) *
+                            (a.dt == 0 ? 2 : 4) / 5e6;
+    double best = 1e30;
+    a.tile = 64;
+    a.splits = 1;
+    for (int edge = 64; edge <= (a.dt == 0 ? 256 : 128); edge *= 2) {
+        const int64_t tiles = tiles_of(a, edge), most = std::min<int64_t>(std::min<int64_t>(nkb / 2, 512 / tiles), 64);
+        for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
+            const int64_t per = (nkb + s - 1) / s;
+            if (s > 1 && (nkb + per - 1) / per != s) continue;   // it would leave a split empty
+            if ((tiles * s + 7) / 8 * 8 * (edge == 256 ? 512 : 256) >= kGridThreads) continue;
+            double us = std::max(gated_us(a, edge, double(tiles * s) / 256, double(per)), bytes_us);
+            if (s > 1) us += (a.dt == 0 ? 4 : 8) + double(s) * sum_bytes / 1.2e7;
+            if (MUON_LINEAR_EDGE && edge != MUON_LINEAR_EDGE) us += 1e9;
+            if (us < best) {
+                best = us;
+                a.tile = edge;
+                a.splits = int(s);
+            }
+        }
+    }
     a.deep = tiles_of(a, a.tile) * a.splits <= 256;
-    // leading dimensions of the re-laid operands (the plan's, but for K's rounding)
     const int64_t chunk = a.dt == 0 ? 8 : 4, es = a.dt == 0 ? 2 : 4;
     const int64_t ar = a.a_kc ? a.M : a.K, ac = a.a_kc ? a.K : a.M, br = a.b_kc ? a.N : a.K, bc = a.b_kc ? a.K : a.N;
     a.a_ld = a.a_dma ? 0 : (ac + chunk - 1) / chunk * chunk;
@@ -125,10 +186,8 @@ GatedPlan plan_gated(GatedArgs& a) {
     g.a_bytes = size_t(a.a_ld) * size_t(ar) * size_t(es);
     g.b_bytes = size_t(a.b_ld) * size_t(br) * size_t(es);
     if (a.splits > 1) {
-        const OutShape o = out_shape(a);
-        const size_t outs = a.pair == PAIR_COLS || a.pair == PAIR_OUT ? 2 : 1;
-        g.partial_bytes = outs * size_t(a.splits) * size_t(o.rows) * size_t(o.ldp) * 4;
-        g.db_bytes = a.db || a.db2 ? outs * size_t(a.splits) * size_t(a.N) * 4 : 0;
+        g.partial_bytes = size_t(outs) * size_t(a.splits) * size_t(o.rows) * size_t(o.ldp) * 4;
+        g.db_bytes = a.db || a.db2 ? size_t(outs) * size_t(a.splits) * size_t(a.N) * 4 : 0;
     }
     return g;
 }

@@ -207,8 +207,7 @@ struct LinPlan {
     int64_t a_ld = 0, b_ld = 0;
     size_t partial_bytes = 0, db_bytes = 0, a_bytes = 0, b_bytes = 0;
 };
-// relay_only: operands without whole aligned chunks are always re-laid.
-LinPlan plan_linear(const LinArgs& a, bool relay_only = false);
+LinPlan plan_linear(const LinArgs& a);
 hipError_t launch_linear(const LinArgs& a, hipStream_t s);
 // A copy of a matrix with rows of whole aligned 16-byte chunks, their ends zero.
 hipError_t launch_pack(const void* src, int64_t ld, void* dst, int64_t ldd, int64_t rows, int64_t cols, int dt,

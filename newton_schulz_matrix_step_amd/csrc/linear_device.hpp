@@ -363,13 +363,31 @@ __device__ __forceinline__ float group_max(const float (&v)[8], int nv) {
     float m = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = max_mag(m, k < nv ? v[k] : 0.f);
-    m = max_mag(m, __shfl_xor(m, SH, 64));
-    return max_mag(m, __shfl_xor(m, 2 * SH, 64));
+    if constexpr (SH == 16) {            // lanes 16 and 32 apart: swapped, without LDS
+        typedef unsigned u2 __attribute__((ext_vector_type(2)));
+        const u2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+        m = max_mag(__uint_as_float(s[0]), __uint_as_float(s[1]));
+        const u2 t = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+        return max_mag(__uint_as_float(t[0]), __uint_as_float(t[1]));
+    } else {
+        m = max_mag(m, __shfl_xor(m, SH, 64));
+        return max_mag(m, __shfl_xor(m, 2 * SH, 64));
+    }
 }
+// act8_code of 8 values as bytes.  1.5 * 2^23 + x, |x| <= 127, is rounded to an
+// integer (nearest, halves to even), whose two's complement is its low bits.
 __device__ __forceinline__ u32x2_t act8_pack(const float (&v)[8], uint32_t e, int nv) {
-    u32x2_t w = {0u, 0u};
+    const bool bad = e == 255u;
+    const float inv = bad ? 0.f : act8_inv(e);
+    u32x2_t w;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k >> 2] |= (k < nv ? act8_code(v[k], e) : 0u) << (8 * (k & 3));
+    for (int h = 0; h < 2; ++h) {
+        uint32_t b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            b[k] = __float_as_uint(fmaf(4 * h + k < nv ? v[4 * h + k] : 0.f, inv, 12582912.f)) & 0xFFu;
+        w[h] = bad ? 0u : b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);   // (a NaN's product is one)
+    }
     return w;
 }
 __device__ __forceinline__ void act_all(float (&v)[8], int act) {
@@ -514,17 +532,47 @@ __device__ __forceinline__ void epilogue_run(const LinArgs& a, const RunAt& t, f
 }
 
 // ---- the gated feed-forward's epilogues ----
-// The values z's run stands for, from its full or its 8-bit copy.
+// Both pre-activations of a run as loaded (full, or codes and exponent byte), and
+// the values they stand for.
 template <int DT>
-__device__ __forceinline__ void z_load(const void* z, int64_t ld, const Act8View& z8, const RunAt& t, float (&v)[8]) {
-    if (z) {
-        run_load<DT>(z, ld, t, DT, v);
+struct ZRaw {
+    u32x4_t g, u, g1, u1;      // g1, u1: the second halves of float32 runs
+};
+template <int DT>
+__device__ __forceinline__ void z_fetch(const GatedArgs& a, const RunAt& t, ZRaw<DT>& w) {
+    if (a.z) {
+        const GMEM char* g = run_ptr(static_cast<const char*>(a.z), a.ld_z, t, DT == 0 ? 2 : 4);
+        const GMEM char* u = run_ptr(static_cast<const char*>(a.z2), a.ld_z, t, DT == 0 ? 2 : 4);
+        w.g = *reinterpret_cast<const GMEM u32x4_t*>(g);
+        w.u = *reinterpret_cast<const GMEM u32x4_t*>(u);
+        if constexpr (DT == 1) {
+            w.g1 = *reinterpret_cast<const GMEM u32x4_t*>(g + 16);
+            w.u1 = *reinterpret_cast<const GMEM u32x4_t*>(u + 16);
+        }
         return;
     }
-    const float step = act8_step(*run_ptr(z8.exps, z8.lde, RunAt{t.r, t.c / kAct8Group, t.rl, t.cl / kAct8Group}, 1));
-    const u32x2_t w = *reinterpret_cast<const GMEM u32x2_t*>(run_ptr(z8.codes, z8.ld, t, 1));
-    act8_dec4(w[0], step, v);
-    act8_dec4(w[1], step, v + 4);
+    auto get = [&](const Act8View& q) {
+        const u32x2_t c = *reinterpret_cast<const GMEM u32x2_t*>(run_ptr(q.codes, q.ld, t, 1));
+        return u32x4_t{c[0], c[1], *run_ptr(q.exps, q.lde, RunAt{t.r, t.c / kAct8Group, t.rl, t.cl / kAct8Group}, 1), 0u};
+    };
+    w.g = get(a.z8);
+    w.u = get(a.z8_2);
+}
+template <int DT>
+__device__ __forceinline__ void z_values(bool full, u32x4_t w, u32x4_t w1, float (&v)[8]) {
+    if (!full) {
+        const float step = act8_step(w[2]);
+        act8_dec4(w[0], step, v);
+        act8_dec4(w[1], step, v + 4);
+    } else if constexpr (DT == 0) {
+        unpack_bf16x8(w, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = __uint_as_float(w[k]);
+            v[4 + k] = __uint_as_float(w1[k]);
+        }
+    }
 }
 template <int DT>
 __device__ __forceinline__ void z_store(void* z, int64_t ld, const Act8View& z8, const RunAt& t, const float (&v)[8]) {
@@ -560,12 +608,15 @@ __device__ __forceinline__ void gated_run(const GatedArgs& a, const RunAt& t, fl
     gate_all(g, u, a.gate_act);
     run_store<DT>(a.out, a.ld_out, t, DT, g);
 }
-// From dh: the gradients at both pre-activations, and h again.
+// From dh: the gradients at both pre-activations, and h again.  Their stores stay
+// in the caches for the products that read them next: streamed past them the call
+// itself is faster (4001 x 2816, 68 MB written: 57 -> 50 us), a whole feed-forward
+// block slower (4096 x 1024 x 2816, forward and backward: 417 -> 434).
 template <int DT>
-__device__ __forceinline__ void gated_dh_run(const GatedArgs& a, const RunAt& t, float (&v)[8]) {
+__device__ __forceinline__ void gated_dh_run(const GatedArgs& a, const RunAt& t, const ZRaw<DT>& w, float (&v)[8]) {
     float g[8], u[8];
-    z_load<DT>(a.z, a.ld_z, a.z8, t, g);
-    z_load<DT>(a.z2, a.ld_z, a.z8_2, t, u);
+    z_values<DT>(a.z != nullptr, w.g, w.g1, g);
+    z_values<DT>(a.z != nullptr, w.u, w.u1, u);
     gate_grad_all(v, g, u, a.gate_act);      // v: dzg, g: dzu, u: h
     run_store<DT>(a.out, a.ld_out, t, DT, v);
     run_store<DT>(a.out2, a.ld_out, t, DT, g);
@@ -836,12 +887,6 @@ __device__ __forceinline__ TileAt tile_at(const LinArgs& a, int edge) {   // at 
 template <int KIND, int PAIR>
 using ArgsOf = std::conditional_t<(KIND >= LIN_GATED || PAIR != PAIR_NONE), GatedArgs, LinArgs>;
 
-template <int KIND, int DT, class Args>
-__device__ __forceinline__ void fast_run(const Args& a, const RunAt& t, float (&v)[8]) {
-    if constexpr (KIND == LIN_GATED_DH) gated_dh_run<DT>(a, t, v);
-    else epilogue_run<KIND, DT>(a, t, v);
-}
-
 // PAIR_OUT: the tile columns past the first output's are the second's.
 __device__ __forceinline__ void pick_output(GatedArgs& a, TileAt& t, int edge) {
     const int64_t n1 = (a.N + edge - 1) / edge;
@@ -1099,11 +1144,35 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(ArgsOf<KIND, PAIR> 
                 }
             }
     };
+    if constexpr (KIND == LIN_GATED_DH) {
+        if (a.splits == 1 && c0 + W <= o.cols && fast_epilogue(a)) {
+            // the next fragment row's pre-activations are in flight under this one's arithmetic
+            ZRaw<N::dt> z[2][TI / 2];
+            auto at = [&](int i, int p) { return RunAt{r0 + wr + 16 * i, c0 + wc + 32 * p, i16, 8 * g}; };
+            auto fetch = [&](int i) {
+#pragma unroll
+                for (int p = 0; p < TI / 2; ++p)
+                    if (r0 + wr + 16 * i + i16 < o.rows) z_fetch<N::dt>(a, at(i, p), z[i & 1][p]);
+            };
+            fetch(0);
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+                if (i + 1 < TI) fetch(i + 1);
+#pragma unroll
+                for (int p = 0; p < TI / 2; ++p) {
+                    float v[8];
+                    join_tiles(acc[i][2 * p], acc[i][2 * p + 1], v);
+                    if (r0 + wr + 16 * i + i16 < o.rows) gated_dh_run<N::dt>(a, at(i, p), z[i & 1][p], v);
+                }
+            }
+            return;
+        }
+    }
     if (a.splits > 1) {
         runs([&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, RunAt{r0 + r, c0 + c, i16, 8 * g}, v); });
     } else if (KIND >= 0 && c0 + W <= o.cols && fast_epilogue(a)) {
         runs([&](int r, int c, float(&v)[8]) {
-            if (r0 + r + i16 < o.rows) fast_run<KIND, N::dt>(a, RunAt{r0 + r, c0 + c, i16, 8 * g}, v);
+            if (r0 + r + i16 < o.rows) epilogue_run<KIND, N::dt>(a, RunAt{r0 + r, c0 + c, i16, 8 * g}, v);
         });
     } else {
         float* stage = reinterpret_cast<float*>(smem);
@@ -1452,13 +1521,42 @@ __global__ __launch_bounds__(kPpThreads, 2) void linear_pp_kernel(ArgsOf<KIND, P
             }
     };
     const bool fast = c0 + 256 <= o.cols && fast_epilogue(a);
+    if constexpr (KIND == LIN_GATED_DH) {
+        if (a.splits == 1 && fast) {
+            // four runs' pre-activations are in flight under the four before: loaded
+            // where they are used, each run would wait out its own loads (nothing
+            // else runs on the CU)
+            ZRaw<0> z[2][4];
+            auto at = [&](int b, int i) {
+                return RunAt{r0 + (b >> 1) * 128 + wr + 16 * i, c0 + (b & 1) * 128 + wc, i16, 8 * g};
+            };
+            auto in = [&](int b, int i) { return r0 + (b >> 1) * 128 + wr + 16 * i + i16 < o.rows; };
+            auto fetch = [&](int b) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (in(b, i)) z_fetch<0>(a, at(b, i), z[b & 1][i]);
+            };
+            fetch(0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (b < 3) fetch(b + 1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v[8];
+                    join_tiles(acc[b >> 1][b & 1][i][0], acc[b >> 1][b & 1][i][1], v);
+                    if (in(b, i)) gated_dh_run<0>(a, at(b, i), z[b & 1][i], v);
+                }
+            }
+            return;
+        }
+    }
     auto half = [&](auto hh) {
         const int64_t rh = r0 + 128 * decltype(hh)::value;
         if (a.splits > 1) {
             runs(hh, [&](int r, int c, float(&v)[8]) { put_partial(a, o, t.split, RunAt{rh + r, c0 + c, i16, 8 * g}, v); });
         } else if (fast) {
             runs(hh, [&](int r, int c, float(&v)[8]) {
-                if (rh + r + i16 < o.rows) fast_run<KIND, 0>(a, RunAt{rh + r, c0 + c, i16, 8 * g}, v);
+                if (rh + r + i16 < o.rows) epilogue_run<KIND, 0>(a, RunAt{rh + r, c0 + c, i16, 8 * g}, v);
             });
         } else {
             float* stage = reinterpret_cast<float*>(smem);

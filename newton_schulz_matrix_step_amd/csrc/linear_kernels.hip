@@ -191,7 +191,7 @@ struct TileCost {
 };
 constexpr TileCost kTileCosts[] = {{64, 3.5, 0.25, 0.40, 0.45}, {128, 5.5, 0.50, 0.75, 1.75}, {256, 11, 1.42, 1.50, 0}};
 
-LinPlan plan_linear(const LinArgs& a, bool relay_only) {
+LinPlan plan_linear(const LinArgs& a) {
     LinPlan best;
     double best_us = 1e30;
     const OutShape o = out_shape(a);
@@ -204,7 +204,7 @@ LinPlan plan_linear(const LinArgs& a, bool relay_only) {
     // operands taken as they are (0), or those that need it re-laid first (1): an
     // 8-bit one decoded, a ragged or misaligned one packed
     const bool plain = a.a_dma && a.b_dma;
-    for (int relay = relay_only && !plain ? 1 : 0; relay <= (plain ? 0 : 1); ++relay) {
+    for (int relay = 0; relay <= (plain ? 0 : 1); ++relay) {
         const bool fused8 = a.a_exps && !relay, dma = relay || plain;
         double relay_us = 0;
         if (relay && !a.a_dma) relay_us += 4 + double(ar) * double(ac) * es * (a.a_exps ? 1.5 : 2) / 4.5e6;
