@@ -501,7 +501,7 @@ muon_status blocknorm_backward(muon_handle* handle, const muon_blocknorm_grad_ar
     const bool want[4] = {p.dpre_gain != nullptr, p.dpre_bias != nullptr, p.dpost_gain || p.dgate,
                           p.dpost_bias || (p.dgate && p.post_bias)};
     for (int i = 0; i < 4; ++i) a.at[i] = want[i] ? a.sums++ : -1;
-    a.parts = blocknorm_parts(p.rows, int(p.cols));
+    a.parts = blocknorm_parts(a);
     DeviceGuard g(h->device);
     if (!g.ok) return fail(h, MUON_ERR_NO_DEVICE, "cannot select device %d", h->device);
     void* ws = nullptr;

@@ -73,21 +73,25 @@ struct RunRaw {
 };
 
 template <class T, int V, bool STREAM>
+__device__ __forceinline__ typename RunRaw<T, V>::vec run_whole(const GMEM T* p, bool in) {   // zeros where not in
+    typename RunRaw<T, V>::vec w;
+#pragma unroll
+    for (int k = 0; k < RunRaw<T, V>::W; ++k) w[k] = 0u;
+    if (!in) return w;
+    if constexpr (RunRaw<T, V>::W == 4) {    // (the alignment would be lost in a template's type)
+        const GMEM u32x4_any_t* q = reinterpret_cast<const GMEM u32x4_any_t*>(p);
+        w = STREAM ? __builtin_nontemporal_load(q) : *q;
+    } else {
+        const GMEM u32x2_any_t* q = reinterpret_cast<const GMEM u32x2_any_t*>(p);
+        w = STREAM ? __builtin_nontemporal_load(q) : *q;
+    }
+    return w;
+}
+template <class T, int V, bool STREAM>
 __device__ __forceinline__ typename RunRaw<T, V>::vec run_get(const GMEM T* p, int n) {
     using R = RunRaw<T, V>;
-    typename R::vec w;
-    if (n >= V) {
-        if constexpr (R::W == 4) {       // (the alignment would be lost in a template's type)
-            const GMEM u32x4_any_t* q = reinterpret_cast<const GMEM u32x4_any_t*>(p);
-            return STREAM ? __builtin_nontemporal_load(q) : *q;
-        } else {
-            const GMEM u32x2_any_t* q = reinterpret_cast<const GMEM u32x2_any_t*>(p);
-            return STREAM ? __builtin_nontemporal_load(q) : *q;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < R::W; ++k) w[k] = 0u;
-    if (n <= 0) return w;
+    typename R::vec w = run_whole<T, V, STREAM>(p, n >= V);
+    if (n <= 0 || n >= V) return w;
     T t[V];                              // one wait for all: past the end the last one again
 #pragma unroll
     for (int k = 0; k < V; ++k) t[k] = p[k < n ? k : n - 1];
@@ -131,12 +135,20 @@ __device__ __forceinline__ void run_put(GMEM T* p, int n, const typename RunRaw<
         }
         return;
     }
+    // element by element, the run's words moved down as they go (a short loop: the
+    // row's last lane alone comes here)
+    typename R::vec t = w;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        if constexpr (sizeof(T) == 2) p[k] = uint16_t(t[0]);
+        else p[k] = __uint_as_float(t[0]);
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-        if (k < n) {
-            if constexpr (sizeof(T) == 2) p[k] = uint16_t(w[k / 2] >> (16 * (k & 1)));
-            else p[k] = __uint_as_float(w[k]);
+        for (int i = 0; i < R::W; ++i) {
+            const uint32_t next = i + 1 < R::W ? t[i + 1] : 0u;
+            if constexpr (sizeof(T) == 2) t[i] = (t[i] >> 16) | (next << 16);
+            else t[i] = next;
         }
+    }
 }
 
 // ---- rows: run j of a lane at column (j * LANES + lane) * V ----
@@ -149,18 +161,37 @@ struct BlockRow {
     struct Raw {
         typename RunRaw<T, V>::vec w[C];
     };
+    // A run that the row's end cuts is loaded as the row's last V elements and moved
+    // down where it is decoded: loaded element by element it would be put together,
+    // and so waited for, where the loads are issued (8192 x 4095 bf16, backward: 161 us
+    // so, 122 this way).
     template <class T, bool STREAM>
     static __device__ __forceinline__ void load(const void* p, int64_t base, int cols, int lane, bool on, Raw<T>& r) {
         const GMEM char* q = reinterpret_cast<const GMEM char*>(gm(static_cast<const T*>(p)) + base);
 #pragma unroll
         for (int j = 0; j < C; ++j) {    // a scalar base and a 32-bit offset that stays the same from row to row
-            const int c = col(j, lane);
-            r.w[j] = run_get<T, V, STREAM>(reinterpret_cast<const GMEM T*>(q + uint32_t(c) * uint32_t(sizeof(T))),
-                                           on ? cols - c : 0);
+            const int c = col(j, lane), n = cols - c, back = n < V ? V - n : 0;
+            r.w[j] = run_whole<T, V, STREAM>(reinterpret_cast<const GMEM T*>(q + uint32_t(c - back) * uint32_t(sizeof(T))),
+                                             on && n > 0);
         }
     }
     template <class T>
-    static __device__ __forceinline__ void decode(const Raw<T>& r, float (&v)[E]) {
+    static __device__ __forceinline__ void decode(const Raw<T>& r, int cols, int lane, float (&v)[E]) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) run_decode<T, V>(r.w[j], v + j * V);
+        if (cols % V == 0) return;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int n = cols - col(j, lane), back = n > 0 && n < V ? V - n : 0;
+            float* t = v + j * V;
+#pragma unroll
+            for (int s = 1; s < V; s *= 2)
+#pragma unroll
+                for (int k = 0; k < V; ++k) t[k] = back & s ? (k + s < V ? t[k + s] : 0.f) : t[k];
+        }
+    }
+    template <class T>
+    static __device__ __forceinline__ void decode(const Raw<T>& r, float (&v)[E]) {   // as encoded
 #pragma unroll
         for (int j = 0; j < C; ++j) run_decode<T, V>(r.w[j], v + j * V);
     }
@@ -287,6 +318,7 @@ void pick_types(int sdt, int dt, F&& f) {
     else f(float{}, float{});
 }
 constexpr int kBlockRowCols = 8192;
+constexpr int kBlockRowLeast = 8;        // columns: a run of any type
 template <class F>
 void pick_block_row(int cols, F&& f) {
     if (cols <= 512) f(std::integral_constant<int, 1>{});
@@ -299,6 +331,8 @@ inline int block_row_waves(int cols) { return cols <= 512 ? 1 : cols <= 1024 ? 2
 constexpr int kRowElems = 8;             // elements a lane holds of a row
 template <class ST, class BT>
 constexpr int run_width() { return sizeof(ST) == 2 && sizeof(BT) == 2 ? 8 : 4; }
+
+inline bool block_row_fits(int cols) { return cols >= kBlockRowLeast && cols <= kBlockRowCols; }
 
 // 8 columns of a row for the kernels of rows that the registers do not hold
 __device__ __forceinline__ void get8(const void* p, int64_t i, int dt, int n, float (&v)[8]) { load8(p, i, dt, false, n, v); }

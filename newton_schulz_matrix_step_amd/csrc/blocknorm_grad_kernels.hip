@@ -18,7 +18,7 @@ namespace {
 
 // LAYER: means, and the sums Q and D.
 template <class ST, class BT, int NW, bool LAYER>
-__global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_grad_kernel(BlockNormGradArgs a) {
+__global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && NW < 16 ? 2 : 4) void blocknorm_grad_kernel(BlockNormGradArgs a) {
     constexpr int E = kRowElems, RB = block_waves(NW) / NW, NT = block_waves(NW) * 64;
     using G = BlockRow<run_width<ST, BT>(), NW, E>;
     __shared__ float red[2][2][block_waves(NW)];
@@ -32,7 +32,7 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_grad_kernel
     for (int q = 0; q < (LAYER ? 4 : 2); ++q)
 #pragma unroll
         for (int i = 0; i < E; ++i) sum[q][i] = 0.f;
-    const float n = float(a.cols);
+    const float inv_n = 1.f / float(a.cols);
     const int64_t step = int64_t(gridDim.x) * RB;
     typename G::template Raw<BT> ry, ro;
     typename G::template Raw<ST> rs, rd;
@@ -91,12 +91,12 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_grad_kernel
             if (LAYER && a.post == NORM_LAYER) pm = gm(a.post_mean)[row];
         }
         if (a.pre) {
-            G::decode(ry, g);
-            G::decode(rs, h);
+            G::decode(ry, a.cols, lane, g);
+            G::decode(rs, a.cols, lane, h);
         }
         if (a.ds) {
             float t[E];
-            G::decode(rd, t);
+            G::decode(rd, a.cols, lane, t);
 #pragma unroll
             for (int i = 0; i < E; ++i) o[i] = t[i];
         } else {
@@ -117,14 +117,14 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_grad_kernel
                 s[1] = fmaf(g[i], h[i], s[1]);
             }
             sums(s);
-            const float c1 = LAYER && a.pre == NORM_LAYER ? s[0] / n : 0.f, c2 = s[1] / n;
+            const float c1 = LAYER && a.pre == NORM_LAYER ? s[0] * inv_n : 0.f, c2 = s[1] * inv_n;
 #pragma unroll
             for (int i = 0; i < E; ++i) g[i] = fmaf(r, g[i] - c1 - h[i] * c2, o[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < E; ++i) g[i] = o[i];
         }
-        if (has_o) G::decode(ro, o);
+        if (has_o) G::decode(ro, a.cols, lane, o);
         // (ds may be dx: another row's, not yet written)
         load(row + step);
         typename G::template Raw<ST> out;
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_grad_kernel
                 }
             if (a.post) {
                 sums(s);
-                const float c1 = LAYER && a.post == NORM_LAYER ? s[0] / n : 0.f, c2 = s[1] / n;
+                const float c1 = LAYER && a.post == NORM_LAYER ? s[0] * inv_n : 0.f, c2 = s[1] * inv_n;
 #pragma unroll
                 for (int i = 0; i < E; ++i) g[i] = pr * (g[i] - c1 - o[i] * c2);
             }
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_grad_kernel
     }
 }
 
-// Rows longer than the registers hold: a workgroup walks rows, 8 columns a lane
+// Rows longer than the registers hold, or shorter than a run: a workgroup walks rows, 8 columns a lane
 // at a time, three passes over each; a lane adds to its own columns' sums in the
 // workgroup's row of partial sums.
 __global__ __launch_bounds__(kNT) void blocknorm_grad_long_kernel(BlockNormGradArgs a) {
@@ -367,23 +367,27 @@ __global__ __launch_bounds__(kNT) void blocknorm_join_kernel(BlockNormGradArgs a
 }
 
 // Two workgroups a CU, each a row of partial sums (8192 x 4096 bf16 RMS 92.6 us; one
-// 110, three 100).
+// 110, three 100); one where a float32 stream's layer norms take the registers of two.
 constexpr int kMaxParts = 512;
+
+bool layer_sums(const BlockNormGradArgs& a) {   // means, or sums that only layer norms have
+    return a.post == NORM_LAYER || a.pre == NORM_LAYER || a.at[1] >= 0 || a.at[3] >= 0;
+}
 
 }  // namespace
 
-int blocknorm_parts(int64_t rows, int cols) {
-    const int w = block_row_waves(cols);
-    const int64_t rb = cols > kBlockRowCols ? 1 : block_waves(w) / w, n = (rows + rb - 1) / rb;
-    return int(n < kMaxParts ? n : kMaxParts);
+int blocknorm_parts(const BlockNormGradArgs& a) {
+    const int w = block_row_waves(a.cols);
+    const int64_t rb = !block_row_fits(a.cols) ? 1 : block_waves(w) / w, n = (a.rows + rb - 1) / rb;
+    const int most = a.sdt == 1 && layer_sums(a) ? kMaxParts / 2 : kMaxParts;
+    return int(n < most ? n : most);
 }
 
 hipError_t launch_blocknorm_grad(const BlockNormGradArgs& a, hipStream_t s) {
     if (a.parts > 0) {
         const dim3 grid{unsigned(a.parts)}, block(kNT);
-        // means or sums that only layer norms have
-        const bool layer = a.post == NORM_LAYER || a.pre == NORM_LAYER || a.at[1] >= 0 || a.at[3] >= 0;
-        if (a.cols > kBlockRowCols) {
+        const bool layer = layer_sums(a);
+        if (!block_row_fits(a.cols)) {
             hipLaunchKernelGGL(blocknorm_grad_long_kernel, grid, block, 0, s, a);
         } else {
             pick_types(a.sdt, a.dt, [&](auto st, auto bt) {

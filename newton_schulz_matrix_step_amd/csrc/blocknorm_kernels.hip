@@ -56,21 +56,30 @@ __device__ __forceinline__ float wave_columns(int cols, int w) {
     return float(n);
 }
 
+// 1 / sqrt(v), within two units in the last place; what the hardware's would flush
+// goes the long way.
+__device__ __forceinline__ float inverse_root(float v) {
+#ifdef __HIP__
+    if (!(v < 1e-37f)) return __builtin_amdgcn_rsqf(v);
+#endif
+    return 1.f / __builtin_sqrtf(v);
+}
+
 // v -> its normalised row (columns past the end become 0); mean and 1 / root.  A
 // layer norm's mean and centred squares are one exchange between the row's waves:
-// each centres its own columns, `here` of them, twice (the mean of what is left
+// each centres its own columns (inv_here: one over their number) twice (the mean of what is left
 // corrects the mean, so that equal values leave nothing, whatever their sum's
 // rounding), and the waves' are joined as those of separate samples, means as
 // differences from the first wave's: M2 = sum of M2_w + n_w (mean_w - mean)^2.
 template <class G, int NW, int E, bool LAYER>
-__device__ __forceinline__ void normalise(float (&v)[E], int kind, float eps, float n, float here, int cols, int lane,
-                                          RowSums<NW>& sums, float& mu, float& r) {
+__device__ __forceinline__ void normalise(float (&v)[E], int kind, float eps, float inv_n, float inv_here,
+                                          int cols, int lane, RowSums<NW>& sums, float& mu, float& r) {
     mu = 0.f;
     float q[2] = {0.f, 0.f};
     if (LAYER && kind == NORM_LAYER) {
 #pragma unroll
         for (int i = 0; i < E; ++i) q[1] += v[i];
-        float part = here > 0.f ? wave_total(q[1]) / here : 0.f;
+        float part = wave_total(q[1]) * inv_here;
         q[1] = 0.f;
 #pragma unroll
         for (int j = 0; j < G::C; ++j)
@@ -82,18 +91,16 @@ __device__ __forceinline__ void normalise(float (&v)[E], int kind, float eps, fl
             }
         q[0] = wave_total(q[0]);
         q[1] = wave_total(q[1]);
-        if (here > 0.f) {
-            const float fix = q[1] / here;
-            part += fix;
-            q[0] = fmaf(-fix, q[1], q[0]);
-            q[0] = q[0] < 0.f ? 0.f : q[0];      // (a NaN stays one)
-        }
+        const float fix = q[1] * inv_here;
+        part += fix;
+        q[0] = fmaf(-fix, q[1], q[0]);
+        q[0] = q[0] < 0.f ? 0.f : q[0];          // (a NaN stays one)
         if constexpr (NW > 1) {
             float w[2] = {q[0], part}, ref;
             sums.exchange(w, &ref);
             // lane i has wave i mod NW's squares and mean; its count from its place
             const float nw = wave_columns<G>(cols, int(threadIdx.x % NW));
-            const float d = nw > 0.f ? w[1] - ref : 0.f, md = turn_total<NW>(nw * d) / n, e = nw > 0.f ? d - md : 0.f;
+            const float d = nw > 0.f ? w[1] - ref : 0.f, md = turn_total<NW>(nw * d) * inv_n, e = nw > 0.f ? d - md : 0.f;
             mu = ref + md;
             q[0] = turn_total<NW>(fmaf(nw * e, e, w[0]));
         } else {
@@ -113,21 +120,21 @@ __device__ __forceinline__ void normalise(float (&v)[E], int kind, float eps, fl
         sums(s);
         q[0] = s[0];
     }
-    r = 1.f / __builtin_sqrtf(q[0] / n + eps);
+    r = inverse_root(fmaf(q[0], inv_n, eps));
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] *= r;
 }
 
 // LAYER: one of the norms is a layer norm (means and biases).
 template <class ST, class BT, int NW, bool LAYER>
-__global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_kernel(BlockNormArgs a) {
+__global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(BT) == 4 && NW < 16 ? 2 : 4) void blocknorm_kernel(BlockNormArgs a) {
     constexpr int E = kRowElems, RB = block_waves(NW) / NW;
     using G = BlockRow<run_width<ST, BT>(), NW, E>;
     __shared__ float red[2][2][block_waves(NW)];
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6)), rg = wave / NW;   // (rows are scalar)
     const int lane = wave % NW * 64 + int(threadIdx.x & 63);
     const Philox m(a.drop);
-    const float n = float(a.cols);   // divided by: the mean of equal values is exact
+    const float inv_n = 1.f / float(a.cols);
     const int64_t step = int64_t(gridDim.x) * RB;
     // two rows' loads are in flight under a third's arithmetic (the first two before
     // the parameters': a call of few rows waits once for all of them)
@@ -166,16 +173,16 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_kernel(Bloc
     G::param(a.pre_gain, a.pdt, a.cols, lane, 1.f, wn);
     if constexpr (LAYER) G::param(a.pre_bias, a.pdt, a.cols, lane, 0.f, bn);
     RowSums<NW> sums{red, wave};
-    const float here = wave_columns<G>(a.cols, wave % NW);
+    const float here = wave_columns<G>(a.cols, wave % NW), inv_here = here > 0.f ? 1.f / here : 0.f;
     auto one = [&](int64_t row, typename G::template Raw<ST>& x, typename G::template Raw<BT>& o) {
         const bool on = row < a.rows;
         float v[E], t[E], mu, r;
-        G::decode(x, v);
-        if (a.branch) G::decode(o, t);
+        G::decode(x, a.cols, lane, v);
+        if (a.branch) G::decode(o, a.cols, lane, t);
         load(row + 2 * step, x, o);
         if (a.branch) {
             if (a.post) {
-                normalise<G, NW, E, LAYER>(t, a.post, a.post_eps, n, here, a.cols, lane, sums, mu, r);
+                normalise<G, NW, E, LAYER>(t, a.post, a.post_eps, inv_n, inv_here, a.cols, lane, sums, mu, r);
                 if (on && lane == 0) {
                     if (a.post_mean) gm(a.post_mean)[row] = mu;
                     if (a.post_rstd) gm(a.post_rstd)[row] = r;
@@ -195,7 +202,7 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_kernel(Bloc
             G::decode(rs, v);
         }
         if (!a.pre) return;
-        normalise<G, NW, E, LAYER>(v, a.pre, a.pre_eps, n, here, a.cols, lane, sums, mu, r);
+        normalise<G, NW, E, LAYER>(v, a.pre, a.pre_eps, inv_n, inv_here, a.cols, lane, sums, mu, r);
         if (on && lane == 0) {
             if (a.pre_mean) gm(a.pre_mean)[row] = mu;
             if (a.pre_rstd) gm(a.pre_rstd)[row] = r;
@@ -216,7 +223,7 @@ __global__ __launch_bounds__(block_waves(NW) * 64, 4) void blocknorm_kernel(Bloc
     }
 }
 
-// Rows longer than the registers hold: a workgroup walks rows, 8 columns a lane
+// Rows longer than the registers hold, or shorter than a run: a workgroup walks rows, 8 columns a lane
 // at a time, and passes over each as often as it needs (from the caches).
 __global__ __launch_bounds__(kNT) void blocknorm_long_kernel(BlockNormArgs a) {
     __shared__ float red[kWaves];
@@ -323,7 +330,7 @@ constexpr int kMaxLongBlocks = 1024;
 
 hipError_t launch_blocknorm(const BlockNormArgs& a, hipStream_t s) {
     if (a.rows <= 0) return hipSuccess;
-    if (a.cols > kBlockRowCols) {
+    if (!block_row_fits(a.cols)) {
         const int64_t nb = a.rows < kMaxLongBlocks ? a.rows : kMaxLongBlocks;
         hipLaunchKernelGGL(blocknorm_long_kernel, dim3(unsigned(nb)), dim3(kNT), 0, s, a);
         return hipGetLastError();

@@ -145,7 +145,7 @@ struct BlockNormGradArgs {
     int32_t at[4];             // place of each sum in `partial`, -1: not wanted
     int32_t sums;              // how many are
 };
-int blocknorm_parts(int64_t rows, int cols);   // rows of partial sums
+int blocknorm_parts(const BlockNormGradArgs& a);   // rows of partial sums
 hipError_t launch_blocknorm(const BlockNormArgs& a, hipStream_t s);
 hipError_t launch_blocknorm_grad(const BlockNormGradArgs& a, hipStream_t s);
 
