@@ -643,7 +643,8 @@ muon_status muon_dropout(muon_handle *h, const muon_dropout_args *args, void *st
  *
  * in one pass over the rows.  Without a branch it is the norm before the first
  * block (residual_scale 1, no post norm, gate or dropout); with pre_norm NONE it
- * ends behind the last one.  An absent gain or gate is 1, an absent bias 0. */
+ * ends behind the last one.  An absent gain or gate is 1, an absent bias 0.
+ * Squares past float32's range make a row's root infinite. */
 muon_status muon_blocknorm_forward(muon_handle *h, const muon_blocknorm_args *args, void *stream);
 
 /* Its gradient: with g = ds + (the gradient of norm_pre at s), e = branch_scale

@@ -1203,22 +1203,26 @@ def muon_blocknorm_forward(handle: int, x, branch=None, s=None, y=None, post_nor
     f32 = k.torch.f32
 
     def par(nm, t):
-        return None if t is None else k.vector(nm, t, c, pt, "another parameter")
+        return k.vector(nm, t, c, pt, "another parameter")
 
     def stat(nm, t):
-        return None if t is None else k.vector(nm, t, r, f32)
+        return k.vector(nm, t, r, f32)
 
     px, ldx = k.matrix("x", x, shape, st, "x")
     pb, ldb = k.matrix("branch", branch, shape, dt, "branch")
     ps, lds = k.matrix("s", s, shape, st, "x")
     py, ldy = k.matrix("y", y, shape, dt, "branch")
-    a = muon_blocknorm_args(px, pb, par("post_gain", post_gain), par("post_bias", post_bias), par("gate", gate),
-                            par("pre_gain", pre_gain), par("pre_bias", pre_bias), ps, py, k.act8("y8", y8, shape),
-                            stat("post_mean", post_mean), stat("post_rstd", post_rstd), stat("pre_mean", pre_mean),
-                            stat("pre_rstd", pre_rstd), _NO_DROPOUT if drop is None else drop._c(k), r, c, ldx, ldb, lds,
-                            ldy, residual_scale, branch_scale, post_eps, pre_eps,
-                            _code(k.what, NORMS, post_norm, "post_norm"), _code(k.what, NORMS, pre_norm, "pre_norm"), sc,
-                            dc, pc, 0)
+    a = muon_blocknorm_args(
+        px, pb, None if post_gain is None else par("post_gain", post_gain),
+        None if post_bias is None else par("post_bias", post_bias), None if gate is None else par("gate", gate),
+        None if pre_gain is None else par("pre_gain", pre_gain),
+        None if pre_bias is None else par("pre_bias", pre_bias), ps, py, k.act8("y8", y8, shape),
+        None if post_mean is None else stat("post_mean", post_mean),
+        None if post_rstd is None else stat("post_rstd", post_rstd),
+        None if pre_mean is None else stat("pre_mean", pre_mean),
+        None if pre_rstd is None else stat("pre_rstd", pre_rstd), _NO_DROPOUT if drop is None else drop._c(k), r, c,
+        ldx, ldb, lds, ldy, residual_scale, branch_scale, post_eps, pre_eps,
+        _code(k.what, NORMS, post_norm, "post_norm"), _code(k.what, NORMS, pre_norm, "pre_norm"), sc, dc, pc, 0)
     _check(handle, load().muon_blocknorm_forward(handle, a, k.stream(stream)))
 
 
@@ -1241,10 +1245,10 @@ def muon_blocknorm_backward(handle: int, dx, ds=None, dy=None, s=None, branch=No
     f32 = k.torch.f32
 
     def par(nm, t):
-        return None if t is None else k.vector(nm, t, c, pt, "another parameter")
+        return k.vector(nm, t, c, pt, "another parameter")
 
     def stat(nm, t):
-        return None if t is None else k.vector(nm, t, r, f32)
+        return k.vector(nm, t, r, f32)
 
     pdy, lddy = k.matrix("dy", dy, shape, dt, nm)
     pds, ldds = k.matrix("ds", ds, shape, st, "dx")
@@ -1252,14 +1256,21 @@ def muon_blocknorm_backward(handle: int, dx, ds=None, dy=None, s=None, branch=No
     pb, ldb = k.matrix("branch", branch, shape, dt, nm)
     pdx, lddx = k.matrix("dx", dx, shape, st, "dx")
     pdb, lddb = k.matrix("dbranch", dbranch, shape, dt, nm)
-    a = muon_blocknorm_grad_args(pdy, pds, ps, pb, par("post_gain", post_gain), par("post_bias", post_bias),
-                                 par("gate", gate), par("pre_gain", pre_gain), stat("post_mean", post_mean),
-                                 stat("post_rstd", post_rstd), stat("pre_mean", pre_mean), stat("pre_rstd", pre_rstd), pdx,
-                                 pdb, par("dpost_gain", dpost_gain), par("dpost_bias", dpost_bias), par("dgate", dgate),
-                                 par("dpre_gain", dpre_gain), par("dpre_bias", dpre_bias),
-                                 _NO_DROPOUT if drop is None else drop._c(k), r, c, lddy, ldds, lds, ldb, lddx, lddb,
-                                 residual_scale, branch_scale, _code(k.what, NORMS, post_norm, "post_norm"),
-                                 _code(k.what, NORMS, pre_norm, "pre_norm"), sc, dc, pc, 1 if accumulate else 0, 0)
+    a = muon_blocknorm_grad_args(
+        pdy, pds, ps, pb, None if post_gain is None else par("post_gain", post_gain),
+        None if post_bias is None else par("post_bias", post_bias), None if gate is None else par("gate", gate),
+        None if pre_gain is None else par("pre_gain", pre_gain),
+        None if post_mean is None else stat("post_mean", post_mean),
+        None if post_rstd is None else stat("post_rstd", post_rstd),
+        None if pre_mean is None else stat("pre_mean", pre_mean),
+        None if pre_rstd is None else stat("pre_rstd", pre_rstd), pdx, pdb,
+        None if dpost_gain is None else par("dpost_gain", dpost_gain),
+        None if dpost_bias is None else par("dpost_bias", dpost_bias),
+        None if dgate is None else par("dgate", dgate), None if dpre_gain is None else par("dpre_gain", dpre_gain),
+        None if dpre_bias is None else par("dpre_bias", dpre_bias), _NO_DROPOUT if drop is None else drop._c(k), r,
+        c, lddy, ldds, lds, ldb, lddx, lddb, residual_scale, branch_scale,
+        _code(k.what, NORMS, post_norm, "post_norm"), _code(k.what, NORMS, pre_norm, "pre_norm"), sc, dc, pc,
+        1 if accumulate else 0, 0)
     _check(handle, load().muon_blocknorm_backward(handle, a, k.stream(stream)))
 
 

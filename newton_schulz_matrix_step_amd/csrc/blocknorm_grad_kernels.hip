@@ -136,6 +136,11 @@ __global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && N
         if (m.cut) G::mask(m, uint32_t(row), lane, g);
         float w[E];
         factors(1, w);
+        if (has_o && m.cut && !a.post) {
+            // what is dropped adds nothing to the gate's gradient, whatever it was
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = g[i] == 0.f ? 0.f : o[i];
+        }
         if (has_o) {
             float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -270,7 +275,7 @@ __global__ __launch_bounds__(kNT) void blocknorm_grad_long_kernel(BlockNormGradA
             float e[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                o[k] = has_o && k < nv ? (o[k] - pm) * pr : 0.f;
+                o[k] = has_o && k < nv && (a.post || !m.cut || g[k] != 0.f) ? (o[k] - pm) * pr : 0.f;   // (dropped: nothing)
                 e[k] = g[k] * o[k];
             }
             if (sums) {

@@ -496,6 +496,84 @@ def test_blocknorm_constant_and_zero_rows(nsm, h):
         assert bool((y[[0, 1, 2, 4, 5]] == 0).all()) and bool(torch.isnan(y[3, cols // 2])), cols
 
 
+@pytest.mark.parametrize("cols", [6, 520, 4095, 9000])
+def test_dropped_branch_elements_add_nothing(nsm, h, cols):
+    """NaN and infinities where the mask drops: the stream, the branch's gradient and the
+    gate's are as if zeros stood there."""
+    import torch
+    torch.manual_seed(2)
+    rows, p = 12, 0.4
+    keep = torch.from_numpy(bo.dropout_factors(rows, cols, p, 5, 6) != 0).cuda()
+    x, ds, gate = torch.randn(rows, cols, device="cuda"), torch.randn(rows, cols, device="cuda"), torch.randn(cols, device="cuda")
+    clean = torch.randn(rows, cols, device="cuda") * keep
+    bad = torch.where(keep, clean, torch.where(clean.abs().cumsum(1) % 2 > 1, float("nan"), float("inf")))
+    out = []
+    for b in (clean, bad):
+        s, dx, db, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty_like(gate)
+        drop = nsm.Dropout(p, 5, 6)
+        nsm.muon_blocknorm_forward(h, x, branch=b, s=s, gate=gate, drop=drop)
+        nsm.muon_blocknorm_backward(h, dx, ds=ds, branch=b, dbranch=db, gate=gate, dgate=dg, drop=drop)
+        out.append((s, dx, db, dg))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cols", [5, 1000, 9000])
+def test_blocknorm_backward_of_a_plain_residual(nsm, h, cols):
+    """No norms, no gate: the branch itself is not needed, gradients are scaled copies."""
+    import torch
+    ds = torch.randn(7, cols, device="cuda")
+    dx, db = torch.empty_like(ds), torch.empty(7, cols, device="cuda", dtype=torch.bfloat16)
+    nsm.muon_blocknorm_backward(h, dx, ds=ds, dbranch=db, residual_scale=0.5, branch_scale=0.25)
+    assert torch.equal(dx, ds * 0.5) and torch.equal(db, (ds * 0.25).bfloat16())
+
+
+def test_blocknorm_rows_far_apart(nsm, h):
+    """Rows whose offsets pass 2^31 elements, forward and backward."""
+    import torch
+    rows, ld = 70000, 32768
+    big = torch.empty(rows, ld, dtype=torch.bfloat16, device="cuda")
+    x, b, s, y, dx, db = (big[:, 64 * k:64 * k + 24] for k in range(6))
+    x.normal_()
+    b.normal_()
+    r = torch.empty(rows, device="cuda")
+    nsm.muon_blocknorm_forward(h, x, branch=b, s=s, y=y, pre_norm="rms", pre_rstd=r)
+    want = x.float() + b.float()
+    close(host(s), host(want), 2.0 ** -8 * np.abs(host(want)), "s")
+    sv = host(s)
+    xh = sv / np.sqrt((sv ** 2).mean(1, keepdims=True) + 1e-5)
+    close(host(y), xh, (2.0 ** -8 + 2 * depth(24) * U) * np.abs(xh), "y")
+    nsm.muon_blocknorm_backward(h, dx, dy=x, s=s, dbranch=db, pre_norm="rms", pre_rstd=r)
+    g = bo.junction_grad({"pre_rstd": host(r)}, host(x), None, sv, pre="rms")["dx"]
+    close(host(dx), g, 2.0 ** -8 * np.abs(g) + 1e-5 * np.abs(host(r))[:, None] * (1 + np.abs(xh)) * np.abs(host(x)).max(), "dx")
+    assert torch.equal(dx, db)
+
+
+def test_two_handles_on_two_streams(nsm, h):
+    """Blocks that run at one time on handles of their own give what they give alone."""
+    import torch
+    h2 = nsm.muon_init(0)
+    try:
+        a = Block(nsm, h, 700, 512, 1000, "in_out", "silu", 0.1, "rms", "rms", seed=1)
+        b = Block(nsm, h2, 650, 480, 904, "out_in", "gelu", 0.2, "layer", "layer", seed=2)
+        alone = []
+        for x in (a, b):
+            x.run()
+            torch.cuda.synchronize()
+            alone.append(x.outputs())
+        s = [torch.cuda.Stream() for _ in range(2)]
+        for _ in range(4):
+            for x, st in zip((a, b), s):
+                st.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(st):
+                    x.run()
+        torch.cuda.synchronize()
+        for x, want in zip((a, b), alone):
+            assert all(torch.equal(v, want[k]) for k, v in x.outputs().items())
+    finally:
+        nsm.muon_destroy(h2)
+
+
 def test_blocknorm_no_rows(nsm, h):
     import torch
     e = torch.empty(0, 40, device="cuda")
@@ -545,7 +623,7 @@ class Block:
         for k, c in (("n1", n), ("h", f), ("o", n), ("s", n), ("y", n), ("do", n), ("h2", f), ("dzg", f), ("dzu", f), ("dn1", n),
                      ("dxr", n), ("dx", n)):
             t[k] = out(rows, c)
-        for k in ("r1", "rp", "r2", "m1", "m2"):
+        for k in ("r1", "rp", "r2", "m1", "m2", "mp"):
             t[k] = out(rows, dt=torch.float32)
         for k in ("wg", "wu", "wd", "g1", "g2", "pg", "gate"):
             t["d" + k] = torch.empty_like(t[k]) if t[k] is not None else None
@@ -558,7 +636,8 @@ class Block:
         m1, m2 = (t["m1"], t["m2"]) if lm else (None, None)
         rp = t["rp"] if self.post != "none" else None
         j = dict(post_norm=self.post, post_gain=t["pg"], gate=t["gate"], pre_norm=self.pre, pre_gain=t["g2"], branch_scale=0.5,
-                 drop=self.drop, post_rstd=rp, pre_mean=m2, pre_rstd=t["r2"])
+                 drop=self.drop, post_rstd=rp, post_mean=t["mp"] if self.post == "layer" else None, pre_mean=m2,
+                 pre_rstd=t["r2"])
         nsm.muon_blocknorm_forward(h, t["x"], y=t["n1"], pre_norm=self.pre, pre_gain=t["g1"], pre_mean=m1, pre_rstd=t["r1"],
                                    y8=self.n8)
         nsm.muon_gated_forward(h, t["n1"], t["wg"], t["wu"], t["h"], act=self.act, gate_out=self.zg, up_out=self.zu, w_layout=lay)
