@@ -136,11 +136,6 @@ __global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && N
         if (m.cut) G::mask(m, uint32_t(row), lane, g);
         float w[E];
         factors(1, w);
-        if (has_o && m.cut && !a.post) {
-            // what is dropped adds nothing to the gate's gradient, whatever it was
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = g[i] == 0.f ? 0.f : o[i];
-        }
         if (has_o) {
             float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -150,7 +145,7 @@ __global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && N
                     const int i = j * G::V + k;
                     // past the last column g is not 0 under a layer norm: the sums leave it out by the gain there
                     o[i] = (o[i] - pm) * pr;
-                    sum[1][i] = fmaf(g[i], o[i], sum[1][i]);
+                    sum[1][i] += mul_zero(g[i], o[i]);   // (what is dropped adds nothing, whatever it was)
                     if constexpr (LAYER) sum[3][i] += g[i];
                     g[i] *= w[i];
                     if constexpr (LAYER) s[0] += g[i];
