@@ -611,7 +611,7 @@ __device__ __forceinline__ void gated_run(const GatedArgs& a, const RunAt& t, fl
 // From dh: the gradients at both pre-activations, and h again.  Their stores stay
 // in the caches for the products that read them next: streamed past them the call
 // itself is faster (4001 x 2816, 68 MB written: 57 -> 50 us), a whole feed-forward
-// block slower (4096 x 1024 x 2816, forward and backward: 417 -> 434).
+// block slower (4096 x 1024 x 2816, forward and backward: 392 -> 405).
 template <int DT>
 __device__ __forceinline__ void gated_dh_run(const GatedArgs& a, const RunAt& t, const ZRaw<DT>& w, float (&v)[8]) {
     float g[8], u[8];
