@@ -133,7 +133,13 @@ __global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && N
         G::encode(h, out);
         if (on) G::template store<ST, false>(a.dx, row * a.ld_dx, a.cols, lane, out);
         if (!has_b) continue;
-        if (m.cut) G::mask(m, uint32_t(row), lane, g);
+        if (m.cut) {
+            G::mask(m, uint32_t(row), lane, g);
+            if (!a.post) {               // what is dropped adds nothing, whatever it was (a norm's row is NaN with it)
+#pragma unroll
+                for (int i = 0; i < E; ++i) o[i] = g[i] == 0.f ? 0.f : o[i];
+            }
+        }
         float w[E];
         factors(1, w);
         if (has_o) {
@@ -145,7 +151,7 @@ __global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && N
                     const int i = j * G::V + k;
                     // past the last column g is not 0 under a layer norm: the sums leave it out by the gain there
                     o[i] = (o[i] - pm) * pr;
-                    sum[1][i] += mul_zero(g[i], o[i]);   // (what is dropped adds nothing, whatever it was)
+                    sum[1][i] = fmaf(g[i], o[i], sum[1][i]);
                     if constexpr (LAYER) sum[3][i] += g[i];
                     g[i] *= w[i];
                     if constexpr (LAYER) s[0] += g[i];

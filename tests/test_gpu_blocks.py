@@ -518,6 +518,24 @@ def test_dropped_branch_elements_add_nothing(nsm, h, cols):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("p", [0.0, 0.4])
+@pytest.mark.parametrize("cols", [24, 1000, 9000])
+def test_infinite_gradient_beside_a_zero_branch(nsm, h, cols, p):
+    """Infinity times 0 is NaN where the element is kept, and nothing where it is dropped."""
+    import torch
+    torch.manual_seed(3)
+    rows = 6
+    keep = torch.from_numpy(bo.dropout_factors(rows, cols, p, 7, 8) != 0).cuda()
+    ds, branch = torch.randn(rows, cols, device="cuda"), torch.randn(rows, cols, device="cuda")
+    ds[2, ::3], branch[2, ::3] = float("inf"), 0.0
+    gate = torch.ones(cols, device="cuda")
+    dx, db, dg = torch.empty_like(ds), torch.empty_like(ds), torch.empty_like(gate)
+    nsm.muon_blocknorm_backward(h, dx, ds=ds, branch=branch, dbranch=db, gate=gate, dgate=dg, drop=nsm.Dropout(p, 7, 8))
+    want = torch.zeros(cols, dtype=torch.bool, device="cuda")
+    want[::3] = keep[2, ::3]
+    assert torch.equal(dg.isnan(), want) and not dg.isinf().any()
+
+
 @pytest.mark.parametrize("cols", [5, 1000, 9000])
 def test_blocknorm_backward_of_a_plain_residual(nsm, h, cols):
     """No norms, no gate: the branch itself is not needed, gradients are scaled copies."""
