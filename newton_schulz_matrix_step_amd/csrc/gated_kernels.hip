@@ -114,7 +114,7 @@ int64_t gated_tiles128(const GatedArgs& a) { return tiles_of(a, 128); }
 
 // Tile edge and split: the cheapest by a model of the product's time in us, fitted
 // to the four products at ten sizes each in both weight layouts, bf16, on one
-// MI355X (float32: at eight).  With w workgroups a CU and `per` k blocks of 128
+// MI355X (float32: at six).  With w workgroups a CU and `per` k blocks of 128
 // bytes a row in each:
 //
 //   edge 64    fixed + (block per + tile) max(w, 1)
@@ -148,8 +148,14 @@ constexpr GatedCost kInputCost = {4, 0.21, 0.8, 4, 0.56, 8, 0.45, 0.5, 13, 0.95,
 constexpr GatedCost kWeightCost = {4, 0.24, 1.0, 5, 0.60, 8, 0.55, 0.5, 17, 1.5, 0};
 
 double gated_us(const GatedArgs& a, int edge, double w, double per) {
-    if (a.dt != 0)   // float32: bound by the matrix pipes, a CU's workgroups one after the other
-        return edge == 64 ? 4 + (0.58 * per + 1) * std::ceil(w) : w <= 1 ? 6 + 1.75 * per : 8 + 1.9 * per * w;
+    // float32: bound by the matrix pipes, a CU's workgroups one after the other (309 x
+    // 5472 -> 2952 forward: 1.8 workgroups a CU of edge 64 171 us, 1.1 of edge 128 331)
+    if (a.dt != 0) {
+        const bool dh = a.kind == LIN_GATED_DH;
+        const double block = w <= 1 ? 0.66 : a.kind == LIN_GATED ? 0.50 : a.kind == LIN_DW ? 0.57 : 0.53;
+        if (edge == 64) return 4 + (block * per + (dh ? 2.6 : 1)) * std::ceil(w);
+        return 6 + (w <= 1 ? 1.9 * per : 1.85 * per + 2) * std::ceil(w) + (dh ? 16 * std::ceil(w) : 0);
+    }
     const GatedCost& c = a.kind == LIN_GATED ? kForwardCost : a.kind == LIN_GATED_DH ? kHiddenCost
                                                : a.kind == LIN_DX                   ? kInputCost
                                                                                     : kWeightCost;
