@@ -38,22 +38,34 @@ struct Philox {
         }
         return u32x4_t{x0, x1, x2, x3};
     }
-    // v under the mask: a select, so that what is dropped is 0 whatever it was
-    __device__ __forceinline__ float keep(float v, uint32_t word, int half) const {
-        return (half ? word >> 16 : word & 0xFFFFu) < cut ? 0.f : v * scale;
+    __device__ __forceinline__ bool drops(uint32_t word, int half) const {
+        return (half ? word >> 16 : word & 0xFFFFu) < cut;
     }
-    // the V values of the run at column c (a multiple of V)
+    // v under the mask: a select, so that what is dropped is 0 whatever it was
+    __device__ __forceinline__ float keep(float v, uint32_t word, int half) const { return drops(word, half) ? 0.f : v * scale; }
+    // the words of the run of V columns at column c (a multiple of V): half k & 1 of word k / 2
+    template <int V>
+    __device__ __forceinline__ u32x4_t run_words(uint32_t row, uint32_t c) const {
+        const u32x4_t w = words(row, c >> 3);
+        if constexpr (V == 8) return w;
+        const bool hi = (c & 4) != 0;
+        return u32x4_t{hi ? w[2] : w[0], hi ? w[3] : w[1], 0u, 0u};
+    }
+    // that run's V values
     template <int V>
     __device__ __forceinline__ void run(uint32_t row, uint32_t c, float* v) const {
-        const u32x4_t w = words(row, c >> 3);
-        if constexpr (V == 8) {
+        const u32x4_t w = run_words<V>(row, c);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = keep(v[k], w[k >> 1], k & 1);
-        } else {
-            const bool hi = (c & 4) != 0;
-            const uint32_t w0 = hi ? w[2] : w[0], w1 = hi ? w[3] : w[1];
+        for (int k = 0; k < V; ++k) v[k] = keep(v[k], w[k >> 1], k & 1);
+    }
+    // and, unscaled, the values beside them (`beside`), of which what is dropped is 0 too
+    template <int V>
+    __device__ __forceinline__ void run(uint32_t row, uint32_t c, float* v, float* o, bool beside) const {
+        const u32x4_t w = run_words<V>(row, c);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = keep(v[k], k < 2 ? w0 : w1, k & 1);
+        for (int k = 0; k < V; ++k) {
+            v[k] = keep(v[k], w[k >> 1], k & 1);
+            o[k] = beside && drops(w[k >> 1], k & 1) ? 0.f : o[k];
         }
     }
 };
@@ -239,6 +251,10 @@ struct BlockRow {
     static __device__ __forceinline__ void mask(const Philox& m, uint32_t row, int lane, float (&v)[E]) {
 #pragma unroll
         for (int j = 0; j < C; ++j) m.run<V>(row, uint32_t(col(j, lane)), v + j * V);
+    }
+    static __device__ __forceinline__ void mask(const Philox& m, uint32_t row, int lane, float (&v)[E], float (&o)[E], bool beside) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) m.run<V>(row, uint32_t(col(j, lane)), v + j * V, o + j * V, beside);
     }
 };
 

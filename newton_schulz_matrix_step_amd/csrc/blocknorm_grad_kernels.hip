@@ -133,13 +133,8 @@ __global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && N
         G::encode(h, out);
         if (on) G::template store<ST, false>(a.dx, row * a.ld_dx, a.cols, lane, out);
         if (!has_b) continue;
-        if (m.cut) {
-            G::mask(m, uint32_t(row), lane, g);
-            if (!a.post) {               // what is dropped adds nothing, whatever it was (a norm's row is NaN with it)
-#pragma unroll
-                for (int i = 0; i < E; ++i) o[i] = g[i] == 0.f ? 0.f : o[i];
-            }
-        }
+        // what is dropped adds nothing, whatever it was (a norm's row is NaN with it)
+        if (m.cut) G::mask(m, uint32_t(row), lane, g, o, !a.post);
         float w[E];
         factors(1, w);
         if (has_o) {
@@ -268,15 +263,15 @@ __global__ __launch_bounds__(kNT) void blocknorm_grad_long_kernel(BlockNormGradA
         // b and oh of 8 columns from g
         auto post8 = [&](int c, bool sums, float(&g)[8], float(&o)[8]) {
             const int nv = a.cols - c;
-            if (m.cut) m.run<8>(uint32_t(row), uint32_t(c), g);
             float w[8], f[8];
             par8(a.post_gain, c, a.pdt, nv, 1.f, w);
             par8(a.gate, c, a.pdt, nv, 1.f, f);
-            if (has_o) get8(a.branch, row * a.ld_branch + c, a.dt, nv, o);
+            get8(a.branch, row * a.ld_branch + c, a.dt, has_o ? nv : 0, o);
+            if (m.cut) m.run<8>(uint32_t(row), uint32_t(c), g, o, !a.post);   // (dropped: nothing)
             float e[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                o[k] = has_o && k < nv && (a.post || !m.cut || g[k] != 0.f) ? (o[k] - pm) * pr : 0.f;   // (dropped: nothing)
+                o[k] = has_o && k < nv ? (o[k] - pm) * pr : 0.f;
                 e[k] = g[k] * o[k];
             }
             if (sums) {
