@@ -1241,7 +1241,7 @@ def muon_blocknorm_backward(handle: int, dx, ds=None, dy=None, s=None, branch=No
     st, sc = dx.dtype, k.storage("dx", dx)
     nm, block = next(((n, t) for n, t in (("dy", dy), ("branch", branch), ("dbranch", dbranch)) if t is not None), ("", None))
     dt, dc = (st, sc) if block is None else (block.dtype, k.storage(nm, block))
-    pt, pc = _param_type(k, pre_gain, post_gain, gate, dpre_bias)
+    pt, pc = _param_type(k, pre_gain, post_gain, gate, post_bias, dpre_bias)
     f32 = k.torch.f32
 
     def par(nm, t):
