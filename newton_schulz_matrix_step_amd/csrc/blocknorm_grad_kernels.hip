@@ -10,6 +10,9 @@
 //
 // One pass over the rows, HBM bound; a workgroup keeps the column sums of its
 // rows in registers and a second kernel adds the workgroups' in a fixed order.
+// Measured: 8192 x 4096 bf16 RMS 88 us, layer norms 95-99 (the bytes 78.5 at a copy's
+// rate); with a float32 stream 122 and 128-130 (118); 4096 x 8192 with one and layer
+// norms 189-202: sixteen waves spill.
 
 #include "blocknorm_device.hpp"
 
@@ -194,7 +197,9 @@ __global__ __launch_bounds__(block_waves(NW) * 64, LAYER && sizeof(ST) == 4 && N
 
 // Rows longer than the registers hold, or shorter than a run: a workgroup walks rows, 8 columns a lane
 // at a time, three passes over each; a lane adds to its own columns' sums in the
-// workgroup's row of partial sums.
+// workgroup's row of partial sums.  Far from its bytes (4096 x 12288 bf16, RMS 1220 us,
+// layer norms 1490, where the bytes take 118): single elements, and the partial sums
+// read and written for every row.
 __global__ __launch_bounds__(kNT) void blocknorm_grad_long_kernel(BlockNormGradArgs a) {
     __shared__ float red[kWaves];
     const Philox m(a.drop);
@@ -367,8 +372,8 @@ __global__ __launch_bounds__(kNT) void blocknorm_join_kernel(BlockNormGradArgs a
     }
 }
 
-// Two workgroups a CU, each a row of partial sums (8192 x 4096 bf16 RMS 92.6 us; one
-// 110, three 100); one where a float32 stream's layer norms take the registers of two.
+// Two workgroups a CU, each a row of partial sums (8192 x 4096 bf16, RMS 88 us, layer
+// norms 98; one 94 and 107; three 91 and 113); one where a float32 stream's layer norms take the registers of two.
 constexpr int kMaxParts = 512;
 
 bool layer_sums(const BlockNormGradArgs& a) {   // means, or sums that only layer norms have

@@ -11,13 +11,14 @@
 // weight gradient's tiles are both outputs'.  Sums are float32, every result is
 // rounded once.
 //
-// Measured, bf16 (1 MI355X; HBM copies 5.1 TB/s): forward of 1 token 4096 -> 14336
-// 45 us, both weights at 5.2 TB/s; of 4096 tokens 714-758 us, 1.27-1.35 PFLOP/s,
+// Measured, bf16 (MI355X; HBM copies 4.7-5.1 TB/s): forward of 1 token 4096 -> 14336
+// 45-52 us on several cards, both weights, out x in, at 4.5-5.2 TB/s (in x out 69: a
+// tile's row of k is 64 bytes of each); of 4096 tokens 714-758 us, 1.27-1.35 PFLOP/s,
 // matrix pipes busy 69 %.  Smaller products are bound by one or two rounds of tiles
 // and their epilogues: hidden gradient of 4001 x 2816 <- 1024 with 8-bit
-// pre-activations 57 us (29 with a k of 64: half is prologue and epilogue, with 92
-// MB through 176 workgroups, one a CU), input gradient of 8192 x 1024 <- 2816 90-95
-// (the join of two splits 14), both weight gradients of 8192 x 2048 -> 1408 118-122
+// pre-activations 55-61 us, with full ones 57 (29 with a k of 64: half is prologue and
+// epilogue, with 92 MB through 176 workgroups, one a CU), input gradient of 8192 x 1024 <- 2816 90-95
+// (the join of two splits 14), both weight gradients of 8192 x 2048 -> 1408 117-122
 // (352 tiles; decoding x 11).
 
 #include "linear_device.hpp"
@@ -130,7 +131,10 @@ int64_t gated_tiles128(const GatedArgs& a) { return tiles_of(a, 128); }
 // 53.5.  A split adds the joining kernel (4 us and its sums' bytes, which the
 // caches hold: 14 us for two splits of 8192 x 1024).
 // Operands without whole aligned chunks are always copied first to rows that have
-// them, 8-bit ones decoded.
+// them, 8-bit ones decoded: the pairs' kernels have no other source.  It costs most
+// where the weights' bytes bound the call (1 token 4096 -> 14335, in x out: 220 us,
+// aligned 69; 4095 -> 14335, out x in: 199, aligned 46).  The model leaves it out, as
+// it falls on every tile and split alike.
 // MUON_LINEAR_EDGE fixes the edge where that tile can serve the call (a host
 // build for bounds checking runs each kernel on small sizes); 0: by the model.
 #ifndef MUON_LINEAR_EDGE
